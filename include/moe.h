@@ -289,10 +289,126 @@ MOE_API int moe_route_static(const uint16_t *x_bf16, int T, int d_model, const f
                              const float *router_bias, int n_experts, int top_k, int32_t *ids,
                              float *w, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Dense gated feed-forward: the block of a layer that has no experts (the
+ * pages' model is sparse throughout; its shared expert is such a block in
+ * another format), in 16 bits for training and prompts and in 8-bit integers
+ * for serving, and the 8-bit product it stands on.  These calls are stateless:
+ * the caller owns weights, activations and workspace, and nothing is kept from
+ * one call for the next.
+ *
+ *   g = x Wg^T   u = x Wu^T   h = act(g) * u   y = h Wd^T
+ *
+ * Common rules.  All pointers are device memory of one device, which the call
+ * makes current for its own duration (found from its first data pointer); the
+ * stream belongs to that device (NULL = its default stream).  Every matrix is
+ * row-major; ld_* is the distance of two rows in elements, 0 for the row's
+ * length.  Matrix pointers are 16-byte aligned and row distances multiples of
+ * 16 bytes (MOE_ERR_INVALID_ARG otherwise).  Weights, scales and saved
+ * matrices without an ld are contiguous.  Outputs must not overlap inputs or
+ * each other.  Rows behind the last (padding of a larger buffer, columns
+ * between d and ld) are not written.  The calls are asynchronous, allocate
+ * nothing, and can be captured into a CUDA graph.  `workspace` is scratch of
+ * at least the size that the *_workspace call names (256-byte aligned;
+ * contents undefined before and after); calls that can run at the same time,
+ * captured graphs among them, need a workspace each.  Sums are held in 32 bits
+ * (fp32, exact int32 for 8-bit operands) and results do not depend on timing:
+ * the same call gives the same bits.  Errors: INVALID_ARG (also a workspace
+ * that is too small: moe_last_error() names it), UNSUPPORTED (sizes outside
+ * the limits), CUDA. */
+typedef enum { MOE_BF16 = 1, MOE_FP16 = 2, MOE_FP32 = 3 } moe_dtype;
+typedef enum {
+    MOE_ACT_SILU = 1,       /* z / (1 + e^-z) */
+    MOE_ACT_GELU_TANH = 2,  /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+    MOE_ACT_GELU = 3        /* z (1 + erf(z / sqrt 2)) / 2 */
+} moe_act;
+
+typedef struct {
+    int d_model;            /* d: multiple of 8, 8..65536 */
+    int d_ff;               /* I: multiple of 8, 8..65536 */
+    int dtype;              /* MOE_BF16 or MOE_FP16: activations, weights, gate, up */
+    int act;                /* moe_act */
+    const void *w_gate;     /* [d_ff][d_model] */
+    const void *w_up;       /* [d_ff][d_model] */
+    const void *w_down;     /* [d_model][d_ff] */
+} moe_ffn;
+
+/* Workspace bytes of moe_ffn_forward (backward == 0) or moe_ffn_backward for T
+ * rows; needs no device. */
+MOE_API int moe_ffn_workspace(const moe_ffn *f, int T, int backward, long long *bytes);
+
+/* y [T][d] from x [T][d].  gate and up [T][d_ff] receive g and u (rounded to
+ * dtype) for the backward pass; both or neither.  h is rounded to dtype, the
+ * operand type of the second product; g and u enter it in fp32.  T == 0 is a
+ * no-op. */
+MOE_API int moe_ffn_forward(const moe_ffn *f, const void *x, long long ld_x, int T, void *y, long long ld_y,
+                            void *gate, void *up, void *workspace, long long workspace_bytes, void *stream);
+
+/* Gradients of the block from those of y:  with dh = dy Wd (kept in fp32),
+ *   dg = dh * u * act'(g)   du = dh * act(g)     (rounded to dtype, as h is)
+ *   dx = dg Wg + du Wu   dw_gate = dg^T x   dw_up = du^T x   dw_down = dy^T h
+ * dx [T][d] (NULL: not wanted) in dtype; the weight gradients (all three or
+ * none) in the weights' layout, in dtype, or in fp32 with
+ * MOE_FFN_GRAD_FP32; MOE_FFN_GRAD_ADD adds them to what is there (fp32 only:
+ * sums over micro-batches belong in 32 bits).  T == 0 writes zero weight
+ * gradients (adds nothing under GRAD_ADD). */
+#define MOE_FFN_GRAD_FP32 1
+#define MOE_FFN_GRAD_ADD 2
+MOE_API int moe_ffn_backward(const moe_ffn *f, const void *x, long long ld_x, const void *gate, const void *up,
+                             const void *dy, long long ld_dy, int T, void *dx, long long ld_dx, void *dw_gate,
+                             void *dw_up, void *dw_down, int flags, void *workspace, long long workspace_bytes,
+                             void *stream);
+
+/* Rows of x [rows][cols] (bf16, fp16 or fp32) as 8-bit codes and one scale a
+ * row:  scale = max|x| / 127 (fp32),  q = x / scale, rounded to fp32, then to
+ * the nearest whole number (half to even).  A row of zeros (or one whose scale
+ * underflows to zero) has scale 0 and codes 0; a row with a NaN or an infinity
+ * has scale NaN and codes 0, so that every product of it is NaN.  q
+ * [rows][cols] is contiguous.  x may have any row distance of at least cols
+ * and needs the alignment of its type only. */
+MOE_API int moe_quantize_s8(const void *x, int dtype, long long ld_x, int rows, int cols, int8_t *q, float *scale,
+                            void *stream);
+
+/* y[t][n] = (a_scale[t] * w_scale[n]) * sum_k a[t][k] w[n][k]  (+ bias[n]),
+ * a [T][K] and w [N][K] contiguous 8-bit codes, scales and bias fp32, y
+ * [T][N] in y_dtype (any moe_dtype).  The sum is exact in int32; then fp32,
+ * rounded once.  Limits: K a multiple of 16 up to 65536, N a multiple of 8.
+ * T == 0 is a no-op. */
+MOE_API int moe_matmul_s8_workspace(int T, int N, int K, long long *bytes);
+MOE_API int moe_matmul_s8(const int8_t *a, const float *a_scale, int T, const int8_t *w, const float *w_scale, int N,
+                          int K, const float *bias, void *y, int y_dtype, long long ld_y, void *workspace,
+                          long long workspace_bytes, void *stream);
+
+/* The gated block in 8 bits: weights are codes with one fp32 scale an output
+ * row; x is quantised row by row as moe_quantize_s8 does it, g, u and h are
+ * fp32, and h is quantised row by row for the second product. */
+typedef struct {
+    int d_model;            /* multiple of 16, 16..65536 */
+    int d_ff;               /* multiple of 16, 16..65536 */
+    int dtype;              /* MOE_BF16 or MOE_FP16: x and y */
+    int act;                /* moe_act */
+    const int8_t *w_gate;   /* [d_ff][d_model] */
+    const int8_t *w_up;     /* [d_ff][d_model] */
+    const int8_t *w_down;   /* [d_model][d_ff] */
+    const float *s_gate;    /* [d_ff] */
+    const float *s_up;      /* [d_ff] */
+    const float *s_down;    /* [d_model] */
+} moe_ffn_s8;
+
+MOE_API int moe_ffn_s8_workspace(const moe_ffn_s8 *f, int T, long long *bytes);
+MOE_API int moe_ffn_s8_forward(const moe_ffn_s8 *f, const void *x, long long ld_x, int T, void *y, long long ld_y,
+                               void *workspace, long long workspace_bytes, void *stream);
+
+/* Read (and clear) the error word of the calls above on the current device
+ * (their kernels' bounded waits set it; *code receives 0 or a MOE_ERR_*
+ * value).  Synchronises the device. */
+MOE_API int moe_ffn_get_device_error(int *code);
+
 /* Static text for a status code. */
 MOE_API const char *moe_status_string(int status);
 
-/* Text of the most recent MOE_ERR_CUDA / MOE_ERR_OOM on this host thread. */
+/* Text of the most recent MOE_ERR_CUDA / MOE_ERR_OOM on this host thread (and of
+ * the refusals of the dense feed-forward calls). */
 MOE_API const char *moe_last_error(void);
 
 #ifdef __cplusplus

@@ -35,6 +35,16 @@ MOE_FLAG_TRACE = 4
 MOE_L2_STREAM = 0
 MOE_L2_KEEP_SHARED = 1
 MOE_ROUTE_STATIC_MAX_LOGITS = 65536
+MOE_BF16 = 1
+MOE_FP16 = 2
+MOE_FP32 = 3
+MOE_ACT_SILU = 1
+MOE_ACT_GELU_TANH = 2
+MOE_ACT_GELU = 3
+MOE_FFN_GRAD_FP32 = 1
+MOE_FFN_GRAD_ADD = 2
+DTYPES = {"torch.bfloat16": MOE_BF16, "torch.float16": MOE_FP16, "torch.float32": MOE_FP32}
+ACTS = {"silu": MOE_ACT_SILU, "gelu_tanh": MOE_ACT_GELU_TANH, "gelu": MOE_ACT_GELU}
 FORMATS = {"q4": MOE_Q4B32, "q3": MOE_Q3B32, "q2": MOE_Q2B32}
 
 EXPORTED = [
@@ -42,6 +52,9 @@ EXPORTED = [
     "moe_forward_stack_host", "moe_destroy", "moe_get_device_error",
     "moe_status_string", "moe_last_error", "moe_timing_enable", "moe_timing_read",
     "moe_trace_read", "moe_route_static", "moe_set_l2_policy",
+    "moe_ffn_workspace", "moe_ffn_forward", "moe_ffn_backward", "moe_quantize_s8",
+    "moe_matmul_s8_workspace", "moe_matmul_s8", "moe_ffn_s8_workspace", "moe_ffn_s8_forward",
+    "moe_ffn_get_device_error",
 ]
 
 
@@ -63,6 +76,17 @@ class moe_stack_record(ctypes.Structure):
     _fields_ = [("x_bf16", ctypes.c_void_p), ("y_bf16", ctypes.c_void_p), ("y_f32", ctypes.c_void_p),
                 ("ids", ctypes.c_void_p), ("w", ctypes.c_void_p), ("rows", ctypes.c_void_p),
                 ("n_rows", ctypes.c_int)]
+
+
+class moe_ffn(ctypes.Structure):
+    _fields_ = [("d_model", ctypes.c_int), ("d_ff", ctypes.c_int), ("dtype", ctypes.c_int), ("act", ctypes.c_int),
+                ("w_gate", ctypes.c_void_p), ("w_up", ctypes.c_void_p), ("w_down", ctypes.c_void_p)]
+
+
+class moe_ffn_s8(ctypes.Structure):
+    _fields_ = [("d_model", ctypes.c_int), ("d_ff", ctypes.c_int), ("dtype", ctypes.c_int), ("act", ctypes.c_int),
+                ("w_gate", ctypes.c_void_p), ("w_up", ctypes.c_void_p), ("w_down", ctypes.c_void_p),
+                ("s_gate", ctypes.c_void_p), ("s_up", ctypes.c_void_p), ("s_down", ctypes.c_void_p)]
 
 
 class MoeError(RuntimeError):
@@ -90,6 +114,17 @@ def _load() -> ctypes.CDLL:
                                   ctypes.POINTER(ctypes.c_longlong), ctypes.c_char_p, i]
     L.moe_trace_read.argtypes = [vp, ctypes.POINTER(ctypes.c_ulonglong), i, ctypes.POINTER(i)]
     L.moe_route_static.argtypes = [vp, i, i, vp, vp, i, i, vp, vp, vp]
+    ll, pll = ctypes.c_longlong, ctypes.POINTER(ctypes.c_longlong)
+    pf, p8 = ctypes.POINTER(moe_ffn), ctypes.POINTER(moe_ffn_s8)
+    L.moe_ffn_workspace.argtypes = [pf, i, i, pll]
+    L.moe_ffn_forward.argtypes = [pf, vp, ll, i, vp, ll, vp, vp, vp, ll, vp]
+    L.moe_ffn_backward.argtypes = [pf, vp, ll, vp, vp, vp, ll, i, vp, ll, vp, vp, vp, i, vp, ll, vp]
+    L.moe_quantize_s8.argtypes = [vp, i, ll, i, i, vp, vp, vp]
+    L.moe_matmul_s8_workspace.argtypes = [i, i, i, pll]
+    L.moe_matmul_s8.argtypes = [vp, vp, i, vp, vp, i, i, vp, vp, i, ll, vp, ll, vp]
+    L.moe_ffn_s8_workspace.argtypes = [p8, i, pll]
+    L.moe_ffn_s8_forward.argtypes = [p8, vp, ll, i, vp, ll, vp, ll, vp]
+    L.moe_ffn_get_device_error.argtypes = [ctypes.POINTER(i)]
     L.moe_status_string.argtypes = [i]
     L.moe_status_string.restype = ctypes.c_char_p
     L.moe_last_error.argtypes = []
@@ -97,7 +132,9 @@ def _load() -> ctypes.CDLL:
     for n in ("moe_create", "moe_load_layer", "moe_forward", "moe_forward_stack",
               "moe_forward_stack_host", "moe_destroy", "moe_get_device_error",
               "moe_timing_enable", "moe_timing_read", "moe_trace_read", "moe_route_static",
-              "moe_set_l2_policy"):
+              "moe_set_l2_policy", "moe_ffn_workspace", "moe_ffn_forward", "moe_ffn_backward", "moe_quantize_s8",
+              "moe_matmul_s8_workspace", "moe_matmul_s8", "moe_ffn_s8_workspace", "moe_ffn_s8_forward",
+              "moe_ffn_get_device_error"):
         getattr(L, n).restype = i
     return L
 
@@ -217,3 +254,169 @@ def make_record(x=None, y=None, y_f32=None, ids=None, w=None, rows=None) -> moe_
     r.rows = _ptr(rows)
     r.n_rows = 0 if rows is None else int(rows.numel())
     return r
+
+
+# ---- dense feed-forward (see include/moe.h) ---------------------------------------------------------------------
+# Tensors carry their sizes here: activations are 2-d CUDA tensors whose rows may lie apart (a slice of a wider
+# buffer); everything else is contiguous.  Shapes and types are checked before an address leaves Python.
+
+def _dtype(t) -> int:
+    try:
+        return DTYPES[str(t.dtype)]
+    except KeyError:
+        raise ValueError(f"dtype {t.dtype}: bf16, fp16 or fp32 expected") from None
+
+
+def _rows(t, T: int, cols: int, dtype, what: str):
+    """(address, row distance) of the first T rows of a [>= T][cols] CUDA tensor of the given torch dtype."""
+    if t.dim() != 2 or t.shape[1] != cols or t.shape[0] < T or t.dtype != dtype or not t.is_cuda:
+        raise ValueError(f"{what}: a CUDA tensor [{T}, {cols}] of {dtype} expected")
+    if t.shape[0] <= 1 or T <= 1:
+        ld = 0
+    else:
+        ld = t.stride(0)
+        if ld < cols:
+            raise ValueError(f"{what}: rows overlap")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what}: elements of a row must be contiguous")
+    return t.data_ptr(), ld
+
+
+def _full(t, shape, dtype, what: str):
+    """Address of a contiguous CUDA tensor of this shape and torch dtype."""
+    if tuple(t.shape) != shape or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{what}: a contiguous CUDA tensor {list(shape)} of {dtype} expected")
+    return t.data_ptr()
+
+
+def _space(ws):
+    if ws is None:
+        return None, 0
+    if not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError("workspace: a contiguous CUDA tensor expected")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _act(act) -> int:
+    return ACTS[act] if isinstance(act, str) else int(act)
+
+
+def make_ffn(w_gate, w_up, w_down, act="silu") -> moe_ffn:
+    """The block over its weights [d_ff, d_model], [d_ff, d_model], [d_model, d_ff] (kept alive by the result)."""
+    I, d = w_gate.shape
+    f = moe_ffn()
+    f.d_model, f.d_ff, f.dtype, f.act = d, I, _dtype(w_gate), _act(act)
+    f.torch_dtype = w_gate.dtype
+    f.w_gate = _full(w_gate, (I, d), f.torch_dtype, "w_gate")
+    f.w_up = _full(w_up, (I, d), f.torch_dtype, "w_up")
+    f.w_down = _full(w_down, (d, I), f.torch_dtype, "w_down")
+    f.keep = (w_gate, w_up, w_down)
+    return f
+
+
+def moe_ffn_workspace(f: moe_ffn, T: int, backward: bool = False) -> int:
+    n = ctypes.c_longlong()
+    _check(lib.moe_ffn_workspace(ctypes.byref(f), T, 1 if backward else 0, ctypes.byref(n)), "moe_ffn_workspace")
+    return n.value
+
+
+def moe_ffn_forward(f: moe_ffn, x, T: int, y, gate=None, up=None, workspace=None, stream=None) -> None:
+    dt, d, I = f.torch_dtype, f.d_model, f.d_ff
+    xp, lx = _rows(x, T, d, dt, "x")
+    yp, ly = _rows(y, T, d, dt, "y")
+    gp = None if gate is None else _full(gate, (T, I), dt, "gate")
+    up_ = None if up is None else _full(up, (T, I), dt, "up")
+    wp, wn = _space(workspace)
+    _check(lib.moe_ffn_forward(ctypes.byref(f), xp, lx, T, yp, ly, gp, up_, wp, wn, _stream(stream)),
+           "moe_ffn_forward")
+
+
+def moe_ffn_backward(f: moe_ffn, x, gate, up, dy, T: int, dx=None, dw_gate=None, dw_up=None, dw_down=None,
+                     add: bool = False, workspace=None, stream=None) -> None:
+    """Gradients of the block; fp32 weight-gradient tensors select fp32 sums, ``add`` adds to what they hold."""
+    dt, d, I = f.torch_dtype, f.d_model, f.d_ff
+    xp, lx = (None, 0) if x is None else _rows(x, T, d, dt, "x")
+    dyp, ldy = _rows(dy, T, d, dt, "dy")
+    dxp, ldx = (None, 0) if dx is None else _rows(dx, T, d, dt, "dx")
+    gp, up_ = _full(gate, (T, I), dt, "gate"), _full(up, (T, I), dt, "up")
+    flags = MOE_FFN_GRAD_ADD if add else 0
+    wdt = dt
+    if dw_gate is not None and _dtype(dw_gate) == MOE_FP32:
+        flags |= MOE_FFN_GRAD_FP32
+        wdt = dw_gate.dtype
+    dg = None if dw_gate is None else _full(dw_gate, (I, d), wdt, "dw_gate")
+    du = None if dw_up is None else _full(dw_up, (I, d), wdt, "dw_up")
+    dd = None if dw_down is None else _full(dw_down, (d, I), wdt, "dw_down")
+    wp, wn = _space(workspace)
+    _check(lib.moe_ffn_backward(ctypes.byref(f), xp, lx, gp, up_, dyp, ldy, T, dxp, ldx, dg, du, dd, flags, wp, wn,
+                                _stream(stream)), "moe_ffn_backward")
+
+
+def _codes(t, shape, what: str):
+    if str(t.dtype) != "torch.int8":
+        raise ValueError(f"{what}: int8 expected")
+    return _full(t, shape, t.dtype, what)
+
+
+def _scales(t, n: int, what: str):
+    if str(t.dtype) != "torch.float32":
+        raise ValueError(f"{what}: fp32 expected")
+    return _full(t, (n,), t.dtype, what)
+
+
+def moe_quantize_s8(x, q, scale, stream=None) -> None:
+    """Rows of x (bf16, fp16, fp32) as 8-bit codes q [rows, cols] and scales [rows]."""
+    rows, cols = x.shape
+    xp, lx = _rows(x, rows, cols, x.dtype, "x")
+    _check(lib.moe_quantize_s8(xp, _dtype(x), lx, rows, cols, _codes(q, (rows, cols), "q"),
+                               _scales(scale, rows, "scale"), _stream(stream)), "moe_quantize_s8")
+
+
+def moe_matmul_s8_workspace(T: int, N: int, K: int) -> int:
+    n = ctypes.c_longlong()
+    _check(lib.moe_matmul_s8_workspace(T, N, K, ctypes.byref(n)), "moe_matmul_s8_workspace")
+    return n.value
+
+
+def moe_matmul_s8(a, a_scale, w, w_scale, y, bias=None, workspace=None, stream=None) -> None:
+    """y [T, N] = scaled product of 8-bit a [T, K] and w [N, K], plus bias [N]."""
+    T, K = a.shape
+    N = w.shape[0]
+    yp, ly = _rows(y, T, N, y.dtype, "y")
+    wp, wn = _space(workspace)
+    _check(lib.moe_matmul_s8(_codes(a, (T, K), "a"), _scales(a_scale, T, "a_scale"), T, _codes(w, (N, K), "w"),
+                             _scales(w_scale, N, "w_scale"), N, K, None if bias is None else _scales(bias, N, "bias"),
+                             yp, _dtype(y), ly, wp, wn, _stream(stream)), "moe_matmul_s8")
+
+
+def make_ffn_s8(w_gate, s_gate, w_up, s_up, w_down, s_down, act="silu", dtype=None) -> moe_ffn_s8:
+    """The block over 8-bit weights and their row scales; ``dtype``: torch.bfloat16 or torch.float16 of x and y."""
+    I, d = w_gate.shape
+    f = moe_ffn_s8()
+    f.d_model, f.d_ff, f.dtype, f.act = d, I, DTYPES.get(str(dtype), 0), _act(act)
+    f.torch_dtype = dtype
+    f.w_gate, f.s_gate = _codes(w_gate, (I, d), "w_gate"), _scales(s_gate, I, "s_gate")
+    f.w_up, f.s_up = _codes(w_up, (I, d), "w_up"), _scales(s_up, I, "s_up")
+    f.w_down, f.s_down = _codes(w_down, (d, I), "w_down"), _scales(s_down, d, "s_down")
+    f.keep = (w_gate, s_gate, w_up, s_up, w_down, s_down)
+    return f
+
+
+def moe_ffn_s8_workspace(f: moe_ffn_s8, T: int) -> int:
+    n = ctypes.c_longlong()
+    _check(lib.moe_ffn_s8_workspace(ctypes.byref(f), T, ctypes.byref(n)), "moe_ffn_s8_workspace")
+    return n.value
+
+
+def moe_ffn_s8_forward(f: moe_ffn_s8, x, T: int, y, workspace=None, stream=None) -> None:
+    xp, lx = _rows(x, T, f.d_model, f.torch_dtype, "x")
+    yp, ly = _rows(y, T, f.d_model, f.torch_dtype, "y")
+    wp, wn = _space(workspace)
+    _check(lib.moe_ffn_s8_forward(ctypes.byref(f), xp, lx, T, yp, ly, wp, wn, _stream(stream)),
+           "moe_ffn_s8_forward")
+
+
+def moe_ffn_get_device_error() -> int:
+    code = ctypes.c_int(0)
+    _check(lib.moe_ffn_get_device_error(ctypes.byref(code)), "moe_ffn_get_device_error")
+    return code.value

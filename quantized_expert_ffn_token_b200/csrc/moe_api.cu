@@ -5,6 +5,7 @@
 
 #include <algorithm>
 
+#include "dense.cuh"
 #include "moe_internal.cuh"
 
 namespace qeffn {
@@ -48,6 +49,11 @@ int set_oom(const char *what) {
 int set_too_many(const char *what) {
     snprintf(g_last_error, sizeof(g_last_error), "%s", what);
     return MOE_ERR_TOO_MANY_TOKENS;
+}
+
+int set_error(int status, const char *what) {
+    snprintf(g_last_error, sizeof(g_last_error), "%s", what);
+    return status;
 }
 
 int ctx_alloc(moe_ctx *ctx, void **p, size_t bytes, const char *what) {
