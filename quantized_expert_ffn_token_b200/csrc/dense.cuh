@@ -45,6 +45,7 @@ struct GemmArgs {
 };
 
 int launch_gemm(const GemmArgs &g, cudaStream_t st);
+int read_dense_error(int *code);   // reads and clears the error word of the current device
 int launch_quantize_s8(const void *x, int dtype, long long ld, int rows, int cols, int8_t *q, float *scale,
                        cudaStream_t st);
 

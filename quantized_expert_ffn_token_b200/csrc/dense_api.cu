@@ -337,8 +337,7 @@ int moe_ffn_s8_forward(const moe_ffn_s8 *f, const void *x, long long ld_x, int T
 int moe_ffn_get_device_error(int *code) {
     if (!code) return MOE_ERR_INVALID_ARG;
     QE_CHECK(cudaDeviceSynchronize());
-    *code = 0;
-    return MOE_OK;
+    return read_dense_error(code);
 }
 
 }  // extern "C"
