@@ -12,6 +12,8 @@ from __future__ import annotations
 import ctypes
 import os
 
+import torch
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libqeffn.so")
 
@@ -43,7 +45,7 @@ MOE_ACT_GELU_TANH = 2
 MOE_ACT_GELU = 3
 MOE_FFN_GRAD_FP32 = 1
 MOE_FFN_GRAD_ADD = 2
-DTYPES = {"torch.bfloat16": MOE_BF16, "torch.float16": MOE_FP16, "torch.float32": MOE_FP32}
+DTYPES = {torch.bfloat16: MOE_BF16, torch.float16: MOE_FP16, torch.float32: MOE_FP32}
 ACTS = {"silu": MOE_ACT_SILU, "gelu_tanh": MOE_ACT_GELU_TANH, "gelu": MOE_ACT_GELU}
 FORMATS = {"q4": MOE_Q4B32, "q3": MOE_Q3B32, "q2": MOE_Q2B32}
 
@@ -262,29 +264,31 @@ def make_record(x=None, y=None, y_f32=None, ids=None, w=None, rows=None) -> moe_
 
 def _dtype(t) -> int:
     try:
-        return DTYPES[str(t.dtype)]
+        return DTYPES[t.dtype]
     except KeyError:
         raise ValueError(f"dtype {t.dtype}: bf16, fp16 or fp32 expected") from None
 
 
 def _rows(t, T: int, cols: int, dtype, what: str):
     """(address, row distance) of the first T rows of a [>= T][cols] CUDA tensor of the given torch dtype."""
-    if t.dim() != 2 or t.shape[1] != cols or t.shape[0] < T or t.dtype != dtype or not t.is_cuda:
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != cols or shape[0] < T or t.dtype is not dtype or not t.is_cuda:
         raise ValueError(f"{what}: a CUDA tensor [{T}, {cols}] of {dtype} expected")
-    if t.shape[0] <= 1 or T <= 1:
-        ld = 0
-    else:
-        ld = t.stride(0)
-        if ld < cols:
-            raise ValueError(f"{what}: rows overlap")
-    if cols > 1 and t.stride(1) != 1:
+    if t.is_contiguous():
+        return t.data_ptr(), 0
+    ld, inner = t.stride()
+    if cols > 1 and inner != 1:
         raise ValueError(f"{what}: elements of a row must be contiguous")
+    if T <= 1:
+        return t.data_ptr(), 0
+    if ld < cols:
+        raise ValueError(f"{what}: rows overlap")
     return t.data_ptr(), ld
 
 
 def _full(t, shape, dtype, what: str):
     """Address of a contiguous CUDA tensor of this shape and torch dtype."""
-    if tuple(t.shape) != shape or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+    if t.shape != shape or t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{what}: a contiguous CUDA tensor {list(shape)} of {dtype} expected")
     return t.data_ptr()
 
@@ -311,12 +315,13 @@ def make_ffn(w_gate, w_up, w_down, act="silu") -> moe_ffn:
     f.w_up = _full(w_up, (I, d), f.torch_dtype, "w_up")
     f.w_down = _full(w_down, (d, I), f.torch_dtype, "w_down")
     f.keep = (w_gate, w_up, w_down)
+    f.ref = ctypes.byref(f)
     return f
 
 
 def moe_ffn_workspace(f: moe_ffn, T: int, backward: bool = False) -> int:
     n = ctypes.c_longlong()
-    _check(lib.moe_ffn_workspace(ctypes.byref(f), T, 1 if backward else 0, ctypes.byref(n)), "moe_ffn_workspace")
+    _check(lib.moe_ffn_workspace(f.ref, T, 1 if backward else 0, ctypes.byref(n)), "moe_ffn_workspace")
     return n.value
 
 
@@ -327,7 +332,7 @@ def moe_ffn_forward(f: moe_ffn, x, T: int, y, gate=None, up=None, workspace=None
     gp = None if gate is None else _full(gate, (T, I), dt, "gate")
     up_ = None if up is None else _full(up, (T, I), dt, "up")
     wp, wn = _space(workspace)
-    _check(lib.moe_ffn_forward(ctypes.byref(f), xp, lx, T, yp, ly, gp, up_, wp, wn, _stream(stream)),
+    _check(lib.moe_ffn_forward(f.ref, xp, lx, T, yp, ly, gp, up_, wp, wn, _stream(stream)),
            "moe_ffn_forward")
 
 
@@ -348,20 +353,20 @@ def moe_ffn_backward(f: moe_ffn, x, gate, up, dy, T: int, dx=None, dw_gate=None,
     du = None if dw_up is None else _full(dw_up, (I, d), wdt, "dw_up")
     dd = None if dw_down is None else _full(dw_down, (d, I), wdt, "dw_down")
     wp, wn = _space(workspace)
-    _check(lib.moe_ffn_backward(ctypes.byref(f), xp, lx, gp, up_, dyp, ldy, T, dxp, ldx, dg, du, dd, flags, wp, wn,
+    _check(lib.moe_ffn_backward(f.ref, xp, lx, gp, up_, dyp, ldy, T, dxp, ldx, dg, du, dd, flags, wp, wn,
                                 _stream(stream)), "moe_ffn_backward")
 
 
 def _codes(t, shape, what: str):
-    if str(t.dtype) != "torch.int8":
+    if t.dtype is not torch.int8:
         raise ValueError(f"{what}: int8 expected")
-    return _full(t, shape, t.dtype, what)
+    return _full(t, shape, torch.int8, what)
 
 
 def _scales(t, n: int, what: str):
-    if str(t.dtype) != "torch.float32":
+    if t.dtype is not torch.float32:
         raise ValueError(f"{what}: fp32 expected")
-    return _full(t, (n,), t.dtype, what)
+    return _full(t, (n,), torch.float32, what)
 
 
 def moe_quantize_s8(x, q, scale, stream=None) -> None:
@@ -393,18 +398,19 @@ def make_ffn_s8(w_gate, s_gate, w_up, s_up, w_down, s_down, act="silu", dtype=No
     """The block over 8-bit weights and their row scales; ``dtype``: torch.bfloat16 or torch.float16 of x and y."""
     I, d = w_gate.shape
     f = moe_ffn_s8()
-    f.d_model, f.d_ff, f.dtype, f.act = d, I, DTYPES.get(str(dtype), 0), _act(act)
+    f.d_model, f.d_ff, f.dtype, f.act = d, I, DTYPES.get(dtype, 0), _act(act)
     f.torch_dtype = dtype
     f.w_gate, f.s_gate = _codes(w_gate, (I, d), "w_gate"), _scales(s_gate, I, "s_gate")
     f.w_up, f.s_up = _codes(w_up, (I, d), "w_up"), _scales(s_up, I, "s_up")
     f.w_down, f.s_down = _codes(w_down, (d, I), "w_down"), _scales(s_down, d, "s_down")
     f.keep = (w_gate, s_gate, w_up, s_up, w_down, s_down)
+    f.ref = ctypes.byref(f)
     return f
 
 
 def moe_ffn_s8_workspace(f: moe_ffn_s8, T: int) -> int:
     n = ctypes.c_longlong()
-    _check(lib.moe_ffn_s8_workspace(ctypes.byref(f), T, ctypes.byref(n)), "moe_ffn_s8_workspace")
+    _check(lib.moe_ffn_s8_workspace(f.ref, T, ctypes.byref(n)), "moe_ffn_s8_workspace")
     return n.value
 
 
@@ -412,7 +418,7 @@ def moe_ffn_s8_forward(f: moe_ffn_s8, x, T: int, y, workspace=None, stream=None)
     xp, lx = _rows(x, T, f.d_model, f.torch_dtype, "x")
     yp, ly = _rows(y, T, f.d_model, f.torch_dtype, "y")
     wp, wn = _space(workspace)
-    _check(lib.moe_ffn_s8_forward(ctypes.byref(f), xp, lx, T, yp, ly, wp, wn, _stream(stream)),
+    _check(lib.moe_ffn_s8_forward(f.ref, xp, lx, T, yp, ly, wp, wn, _stream(stream)),
            "moe_ffn_s8_forward")
 
 

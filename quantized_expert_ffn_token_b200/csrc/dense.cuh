@@ -44,7 +44,16 @@ struct GemmArgs {
     bool add = false;             // EPI_STORE with fp32 out: out += C
 };
 
-int launch_gemm(const GemmArgs &g, cudaStream_t st);
+// Position of a product among the kernels of its call.  Inside a call the kernels overlap (programmatic launch): one
+// that has a kernel of the same call before it may load the call's weights before it waits, and one that has a kernel
+// of the same call after it lets that start early.  A call's first kernel is launched plainly and its last one never
+// lets another start, so nothing outside the call sees unfinished results.
+struct Link {
+    bool first = true, last = true;
+};
+constexpr int kFewRows = 32;   // products of at most this many rows stream the weights (dense_rows.cu)
+int launch_gemm(const GemmArgs &g, Link link, cudaStream_t st);
+int launch_rows(const GemmArgs &g, Link link, cudaStream_t st);
 int read_dense_error(int *code);   // reads and clears the error word of the current device
 int launch_quantize_s8(const void *x, int dtype, long long ld, int rows, int cols, int8_t *q, float *scale,
                        cudaStream_t st);

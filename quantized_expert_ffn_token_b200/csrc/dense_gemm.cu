@@ -493,7 +493,8 @@ int read_dense_error(int *code) {
     return MOE_OK;
 }
 
-int launch_gemm(const GemmArgs &g, cudaStream_t st) {
+int launch_gemm(const GemmArgs &g, Link link, cudaStream_t st) {
+    if (g.M <= kFewRows && !g.a_mn && !g.b_mn && g.segs == 1) return launch_rows(g, link, st);
     const int bk = g.type == DT_S8 ? 128 : 64;
     const int cg = g.M > 128 ? 2 : 1;
     Maps m;
