@@ -44,12 +44,12 @@ struct GemmArgs {
     bool add = false;             // EPI_STORE with fp32 out: out += C
 };
 
-// Position of a product among the kernels of its call.  Inside a call the kernels overlap (programmatic launch): one
-// that has a kernel of the same call before it may load the call's weights before it waits, and one that has a kernel
-// of the same call after it lets that start early.  A call's first kernel is launched plainly and its last one never
-// lets another start, so nothing outside the call sees unfinished results.
+// Position of a kernel in its call.  The streaming and quantising kernels let the next kernel start early (programmatic
+// launch), after their own wait for the one before; so when a later kernel of a call runs, everything before the call
+// is complete, and it may load the call's weights before it waits for the call's intermediate results.  A call's first
+// kernel reads nothing before its wait, because the kernel before it may be the one that writes its inputs.
 struct Link {
-    bool first = true, last = true;
+    bool first = true;
 };
 constexpr int kFewRows = 32;   // products of at most this many rows stream the weights (dense_rows.cu)
 int launch_gemm(const GemmArgs &g, Link link, cudaStream_t st);

@@ -1,19 +1,24 @@
 // Matrix products of the dense feed-forward operators on the tensor cores.
 //
-// C [M][N] = A . B^T with fp32 (8-bit operands: int32) accumulators in TMEM.  One persistent kernel, a CTA pair on two
-// SMs per output tile of 256 x 256: each CTA holds 128 rows of A and 128 rows of B of every k step, and the pair's MMA
-// (M = 256, N = 256) reads both halves, so an operand byte is loaded into shared memory once per 256 rows of the other
-// operand.  A k step is 128 bytes of the reduction index (64 16-bit or 128 8-bit values), staged by TMA through a ring
-// of shared-memory stages with the 128-byte swizzle.  Operands may be stored with either index contiguous (the
-// gradients read weights and activations as they lie; the MMA's transpose bits do the rest), and rows, columns and
-// reduction tails past the end read as zeros (TMA) and are clipped on the way out.
+// C [M][N] = A . B^T with fp32 (8-bit operands: int32) accumulators in TMEM.  One persistent kernel.  A tile is 256 rows
+// by C columns on a CTA pair (two SMs; the pair's MMAs have M = 256, each CTA holds 128 rows of A and half of B's rows,
+// so that an operand byte enters shared memory once per 256 rows of the other operand), or 128 rows on one CTA where
+// there are no more rows than that.  A k step is 128 bytes of the reduction index (64 16-bit or 128 8-bit values),
+// staged by TMA through a ring of shared-memory stages with the 128-byte swizzle.  Operands may be stored with either
+// index contiguous (the gradients read weights and activations as they lie; the MMA's transpose bits do the rest), and
+// rows, columns and reduction tails past the end read as zeros (TMA) and are clipped on the way out.
 //
 //   warp 0: TMA producer (one lane)         warp 1: MMA issuer (one lane of the pair's first CTA)
-//   warp 2: TMEM allocation                 warps 4..7: epilogue (TMEM lane quarter = warp % 4)
+//   warp 2: TMEM allocation                 warps 4..11: epilogue (TMEM lane quarter = warp % 4, two warps a quarter)
 //
-// TMEM holds two 256-column accumulators, so a tile's epilogue runs while the next tile's MMAs do.  The gated forward
-// product takes 128 gate columns from the first CTA's B and the 128 up columns of the same index from the second's:
-// column c and column 128 + c of a row meet in one thread.
+// A tile's columns are one or two sub-tiles of W <= 256, an accumulator of W TMEM columns each.  With one sub-tile TMEM
+// holds two tiles' accumulators and the epilogue of a tile runs while the next tile's MMAs do; two sub-tiles serve
+// calls whose tiles then all fit on the device at once.  The gated forward product takes the first half of a sub-tile's
+// B rows from the gate matrix and the second from the up matrix: column c and column W/2 + c of a row meet in one
+// thread.  Calls with few tiles split the reduction index over the CTAs of a cluster: the partial accumulators go to
+// shared memory, and every CTA sums (in split order) and finishes some of the columns.
+//
+// The tile shape comes from a model of the time (choose(), below), not from a table of sizes.
 #include <algorithm>
 
 #include "dense.cuh"
@@ -26,16 +31,15 @@ using namespace dense;
 
 namespace {
 
-constexpr int GT_NT = 256;
-constexpr int GT_N = 256;                   // accumulator columns of a tile
-constexpr int GT_KB = 128;                  // bytes of the reduction index per stage
-constexpr int GT_STAGES = 5;
-constexpr int GT_HALF = 128 * GT_KB;        // 128 operand rows of a stage
-constexpr int GT_STAGE = 2 * GT_HALF;       // A and B of one CTA
-constexpr int GT_EPI_W0 = 4;
-constexpr int GT_BUF = 4096;                // an epilogue warp's store tile: 32 rows of 128 bytes
-constexpr int GT_NBUF = 3;                  // tiles in flight per epilogue warp
-constexpr int GT_SMEM = 1024 + GT_STAGES * GT_STAGE + 4 * GT_NBUF * GT_BUF + 256;
+constexpr int GT_NT = 384;
+constexpr int GT_W = 256;                   // largest sub-tile width; TMEM columns between accumulators
+constexpr int GT_A = 128 * 128;             // bytes of A per stage: 128 rows of one k step
+constexpr int GT_MAX_STAGES = 8;
+constexpr int GT_RING = 177 * 1024;         // bytes of the stage ring
+constexpr int GT_EPI_W0 = 4, GT_EPI_NW = 8;
+constexpr int GT_UNIT = 32;                 // columns an epilogue warp handles at a time
+constexpr int GT_SLOT = 6144;               // an epilogue warp's store tiles: three of 32 rows x 64 bytes (one of fp32)
+constexpr int GT_SMEM = 1024 + GT_RING + GT_EPI_NW * GT_SLOT + 256;
 
 struct Maps {
     CUtensorMap a[2], b[2], out[3];
@@ -44,6 +48,9 @@ struct Maps {
 struct TileArgs {
     int M, N, kblocks, segs;    // kblocks: k steps of one segment
     int tiles_m, tiles_n;
+    int W, subs;                // sub-tile width, sub-tiles per tile
+    int splits, kper;           // reduction splits (CTAs or pairs of a cluster), k steps each
+    int stages, stage_bytes;
     int act;
     int fp16;                   // 16-bit operands (and out1, out2): fp16 rather than bf16
     int out_dtype;
@@ -54,7 +61,7 @@ struct TileArgs {
 };
 
 struct GtBars {
-    uint64_t full[GT_STAGES], empty[GT_STAGES], acc_full[2], acc_empty[2], mma_done;
+    uint64_t full[GT_MAX_STAGES], empty[GT_MAX_STAGES], acc_full[2], acc_empty[2], mma_done;
     uint32_t tmem;
 };
 
@@ -71,16 +78,17 @@ __device__ __forceinline__ float2 unpack16(uint32_t v, int fp16) {
     return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162 *>(&v));
 }
 
-// 32 values of this lane's row into half `half` (32 16-bit columns) of a swizzled 32 x 64 store tile.
-__device__ __forceinline__ void stage16(uint8_t *buf, int lane, int half, const float (&v)[32], int fp16) {
+// 32 values of this lane's row into a 32 x 32 store tile of 64-byte rows (64-byte swizzle: 16-byte part c of row r at
+// part c ^ (r / 2 % 4)).
+__device__ __forceinline__ void stage16(uint8_t *buf, int lane, const float (&v)[32], int fp16) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         const uint4 w = make_uint4(pack16(v[8 * c], v[8 * c + 1], fp16), pack16(v[8 * c + 2], v[8 * c + 3], fp16),
                                    pack16(v[8 * c + 4], v[8 * c + 5], fp16), pack16(v[8 * c + 6], v[8 * c + 7], fp16));
-        *reinterpret_cast<uint4 *>(buf + lane * 128 + (((4 * half + c) ^ (lane & 7)) << 4)) = w;
+        *reinterpret_cast<uint4 *>(buf + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = w;
     }
 }
-// 32 fp32 values: the whole row of a 32 x 32 store tile.
+// 32 fp32 values: the whole 128-byte row (128-byte swizzle).
 __device__ __forceinline__ void stage32(uint8_t *buf, int lane, const float (&v)[32]) {
 #pragma unroll
     for (int c = 0; c < 8; ++c)
@@ -89,13 +97,7 @@ __device__ __forceinline__ void stage32(uint8_t *buf, int lane, const float (&v)
 }
 
 template <bool S8>
-__device__ __forceinline__ void load_acc(uint32_t taddr, float (&v)[32]) {
-    uint32_t r[32];
-    tmem_ld32(taddr, r);
-    tmem_wait();
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = S8 ? (float)(int)r[i] : __uint_as_float(r[i]);
-}
+__device__ __forceinline__ float acc_value(uint32_t r) { return S8 ? (float)(int)r : __uint_as_float(r); }
 
 // v[i] *= rs * cs[n + i]: the scales' product first, as the plain form has it.
 __device__ __forceinline__ void apply_scale(float (&v)[32], float rs, const float *cs, int n, int N) {
@@ -103,308 +105,323 @@ __device__ __forceinline__ void apply_scale(float (&v)[32], float rs, const floa
     for (int i = 0; i < 32; ++i) v[i] *= rs * (n + i < N ? __ldg(cs + n + i) : 0.f);
 }
 
-// The store tiles of one epilogue warp: a ring of GT_NBUF buffers, each free again once its copy has been read.
-struct StoreRing {
-    uint8_t *base;
-    int lane, at = 0;
-    __device__ uint8_t *acquire() {
-        if (lane == 0) tma_wait_read<GT_NBUF - 1>();
-        __syncwarp();
-        return base + at * GT_BUF;
-    }
-    __device__ void release(const CUtensorMap *m, int x, int y, bool in, bool add = false) {
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-            if (in) {
-                if (add) tma_add(m, x, y, base + at * GT_BUF);
-                else tma_store(m, x, y, base + at * GT_BUF);
-            }
-            tma_commit();
-        }
-        at = at + 1 == GT_NBUF ? 0 : at + 1;
-    }
-};
-
 template <bool S8, bool A_MN, bool B_MN, int EPI, int CG>
 __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Maps maps, const __grid_constant__ TileArgs p) {
     constexpr int BK = S8 ? 128 : 64;             // reduction values per stage
     constexpr int TM = 128 * CG;                  // rows of a tile
-    constexpr int B_ROWS = GT_N / CG;             // B rows a CTA holds
-    constexpr int STAGE = GT_HALF + B_ROWS * GT_KB;
-    constexpr int STAGES = CG == 2 ? GT_STAGES : GT_STAGES * GT_STAGE / STAGE;
-    constexpr int TN = EPI == EPI_GATE ? GT_N / 2 : GT_N;   // output columns of a tile
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024 - (su32(smem_raw) & 1023)) & 1023);
-    uint8_t *bufs = smem + GT_STAGES * GT_STAGE;
-    GtBars *bar = reinterpret_cast<GtBars *>(bufs + 4 * GT_NBUF * GT_BUF);
+    uint8_t *slots = smem + GT_RING;
+    GtBars *bar = reinterpret_cast<GtBars *>(slots + GT_EPI_NW * GT_SLOT);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = CG == 2 ? cluster_rank() : 0;
+    const uint32_t crank = cluster_rank();
+    const uint32_t rank = CG == 2 ? crank & 1 : 0, even = crank - rank;   // rank in the pair, the pair's first CTA
+    const int split = crank / CG;
+    const int W = p.W, half = W / 2;
+    const int tile_cols = (EPI == EPI_GATE ? half : W) * p.subs;          // output columns of a tile
+    const bool two_acc = p.subs == 1;                                     // accumulators of two tiles in TMEM
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < STAGES; ++s) {
+        for (int s = 0; s < p.stages; ++s) {
             mbar_init(&bar->full[s], 1);
             mbar_init(&bar->empty[s], 1);
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(&bar->acc_full[t], 1);
-            mbar_init(&bar->acc_empty[t], 4 * CG);
+            mbar_init(&bar->acc_empty[t], GT_EPI_NW * CG);
         }
         mbar_init(&bar->mma_done, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 2) tmem_alloc<CG>(&bar->tmem, 2 * GT_N);
+    if (warp == 2) tmem_alloc<CG>(&bar->tmem, 2 * GT_W);
     tc_fence_before();
     __syncthreads();
-    if constexpr (CG == 2) cluster_sync();
+    if (CG * p.splits > 1) cluster_sync();
     tc_fence_after();
     const uint32_t tmem = bar->tmem;
 
     const int n_tiles = p.tiles_m * p.tiles_n;
-    const int first = blockIdx.x / CG, step = gridDim.x / CG;
-    const int ksteps = p.kblocks * p.segs;
+    const int first = blockIdx.x / (CG * p.splits), step = gridDim.x / (CG * p.splits);
+    const int k_begin = split * p.kper, k_end = min(p.kblocks * p.segs, k_begin + p.kper);
     // tiles in bands of 8 row blocks, so that the tiles in flight share rows of both operands in L2
     auto tile_at = [&](int t, int &m0, int &n0) {
         const int band = t / (8 * p.tiles_n), in = t - band * 8 * p.tiles_n;
         const int rows = min(8, p.tiles_m - 8 * band);
         m0 = (8 * band + in % rows) * TM;
-        n0 = (in / rows) * TN;
+        n0 = (in / rows) * tile_cols;
     };
 
     if (warp == 0) {
         if (lane == 0) {
-            int it = 0;
+            int s = 0, filled = 0;
+            uint32_t phase = 0;
             bool ok = true;
             for (int t = first; t < n_tiles && ok; t += step) {
                 int m0, n0;
                 tile_at(t, m0, n0);
                 m0 += rank * 128;
-                for (int kb = 0; kb < ksteps && ok; ++kb, ++it) {
-                    const int s = it % STAGES;
-                    ok = mbar_wait(&bar->empty[s], ((it / STAGES) & 1) ^ 1);
+                for (int kb = k_begin; kb < k_end; ++kb) {
+                    ok = mbar_wait(&bar->empty[s], phase ^ 1);
                     if (!ok) break;
                     const int seg = kb >= p.kblocks, k0 = (kb - seg * p.kblocks) * BK;
-                    uint8_t *sa = smem + s * STAGE, *sb = sa + GT_HALF;
-                    if (rank == 0) mbar_expect_tx(&bar->full[s], CG * STAGE);
-                    const uint32_t fb = CG == 2 ? map_rank(&bar->full[s], 0) : su32(&bar->full[s]);
+                    uint8_t *sa = smem + s * p.stage_bytes, *sb = sa + GT_A;
+                    if (rank == 0) mbar_expect_tx(&bar->full[s], CG * p.stage_bytes);
+                    const uint32_t fb = CG == 2 ? map_rank(&bar->full[s], even) : su32(&bar->full[s]);
                     const CUtensorMap *ma = &maps.a[seg];
                     if constexpr (A_MN) {
                         tma_load<CG>(sa, ma, m0, k0, fb);
-                        tma_load<CG>(sa + GT_HALF / 2, ma, m0 + 64, k0, fb);
+                        tma_load<CG>(sa + GT_A / 2, ma, m0 + 64, k0, fb);
                     } else {
                         tma_load<CG>(sa, ma, k0, m0, fb);
                     }
-#pragma unroll
-                    for (int h = 0; h < B_ROWS / 128; ++h) {   // 128 rows of B each: which half of the tile
-                        const int half = CG == 2 ? rank : h;
-                        const CUtensorMap *mb = EPI == EPI_GATE ? &maps.b[half] : &maps.b[seg];
-                        const int nb = EPI == EPI_GATE ? n0 : n0 + 128 * half;
-                        uint8_t *dst = sb + h * GT_HALF;
+                    auto load_b = [&](int sub, int h) {   // half h of a sub-tile's rows
+                        const CUtensorMap *mb = EPI == EPI_GATE ? &maps.b[h] : &maps.b[seg];
+                        const int nb = EPI == EPI_GATE ? n0 + sub * half : n0 + sub * W + h * half;
                         if constexpr (B_MN) {
-                            tma_load<CG>(dst, mb, nb, k0, fb);
-                            tma_load<CG>(dst + GT_HALF / 2, mb, nb + 64, k0, fb);
+                            for (int c = 0; c < half; c += 64, sb += 64 * 128) tma_load<CG>(sb, mb, nb + c, k0, fb);
                         } else {
-                            tma_load<CG>(dst, mb, k0, nb, fb);
+                            tma_load<CG>(sb, mb, k0, nb, fb);
+                            sb += half * 128;
                         }
+                    };
+                    if constexpr (CG == 2) {
+                        load_b(0, rank);
+                        if (p.subs == 2) load_b(1, rank);
+                    } else {
+                        load_b(0, 0);
+                        load_b(0, 1);
+                        if (p.subs == 2) load_b(1, 0), load_b(1, 1);
                     }
+                    ++filled;
+                    if (++s == p.stages) s = 0, phase ^= 1;
                 }
             }
             // every copy has landed before the CTAs leave: the last fills that no MMA waited for
             if (!ok && rank == 0)
-                for (int j = it - 1; j >= 0 && j >= it - STAGES; --j)
-                    mbar_wait(&bar->full[j % STAGES], (j / STAGES) & 1, true);
+                for (int j = 0; j < p.stages && j < filled; ++j) {
+                    if (s == 0) s = p.stages, phase ^= 1;
+                    --s;
+                    mbar_wait(&bar->full[s], phase, true);
+                }
         }
         __syncwarp();
     } else if (warp == 1) {
         if (rank == 0 && lane == 0) {
             const uint32_t idesc = (S8 ? (2u << 4) | (1u << 7) | (1u << 10)
                                        : (1u << 4) | (p.fp16 ? 0u : (1u << 7) | (1u << 10))) |
-                                   (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u) | ((uint32_t)(GT_N >> 3) << 17) |
+                                   (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u) | ((uint32_t)(W >> 3) << 17) |
                                    ((uint32_t)(TM >> 4) << 24);
-            int it = 0, n = 0;
+            int s = 0, n = 0;
+            uint32_t phase = 0;
             bool ok = true;
             for (int t = first; t < n_tiles && ok; t += step, ++n) {
-                ok = mbar_wait(&bar->acc_empty[n & 1], ((n >> 1) & 1) ^ 1);
+                const int slot = two_acc ? n & 1 : 0, use = two_acc ? n >> 1 : n;
+                ok = mbar_wait(&bar->acc_empty[slot], (use & 1) ^ 1);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t acc = tmem + GT_N * (n & 1);
-                for (int kb = 0; kb < ksteps; ++kb, ++it) {
-                    const int s = it % STAGES;
-                    ok = mbar_wait(&bar->full[s], (it / STAGES) & 1);
+                for (int kb = k_begin; kb < k_end; ++kb) {
+                    ok = mbar_wait(&bar->full[s], phase);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t a0 = su32(smem + s * STAGE), b0 = a0 + GT_HALF;
+                    // 32 bytes of k at a time: within the 128-byte rows, or 16 of the 128-byte rows
+                    const uint32_t a0 = su32(smem + s * p.stage_bytes), acc = tmem + GT_W * slot;
+                    const uint64_t ad = smem_desc(a0, A_MN ? 64 * 128 : 16), bd = smem_desc(a0 + GT_A, B_MN ? 64 * 128 : 16);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        // 32 bytes of k: within the 128-byte rows, or 16 of the 128-byte rows
-                        const uint64_t ad = A_MN ? smem_desc(a0 + 2048 * j, GT_HALF / 2) : smem_desc(a0 + 32 * j, 16);
-                        const uint64_t bd = B_MN ? smem_desc(b0 + 2048 * j, GT_HALF / 2) : smem_desc(b0 + 32 * j, 16);
-                        umma<S8, CG>(acc, ad, bd, idesc, (kb | j) != 0);
+                    for (int j = 0; j < 4; ++j)
+                        umma<S8, CG>(acc, ad + (A_MN ? 128 : 2) * j, bd + (B_MN ? 128 : 2) * j, idesc, kb > k_begin || j > 0);
+                    if (p.subs == 2) {
+                        const uint64_t b1 = bd + ((uint32_t)(W / CG) * 128 >> 4);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            umma<S8, CG>(acc + GT_W, ad + (A_MN ? 128 : 2) * j, b1 + (B_MN ? 128 : 2) * j, idesc, kb > k_begin || j > 0);
                     }
-                    umma_commit<CG>(&bar->empty[s]);
+                    umma_commit<CG>(&bar->empty[s], even);
+                    if (++s == p.stages) s = 0, phase ^= 1;
                 }
-                if (ok) umma_commit<CG>(&bar->acc_full[n & 1]);
+                if (ok) umma_commit<CG>(&bar->acc_full[slot], even);
             }
-            umma_commit<CG>(&bar->mma_done);   // no MMA may still use shared memory or TMEM when the CTAs leave
+            umma_commit<CG>(&bar->mma_done, even);   // no MMA may still use shared memory or TMEM when the CTAs leave
             mbar_wait(&bar->mma_done, 0, true);
         }
         __syncwarp();
-    } else if (warp >= GT_EPI_W0) {
-        const int q = warp - GT_EPI_W0;
-        StoreRing ring{bufs + q * GT_NBUF * GT_BUF, lane};
-        const uint32_t empty0 = CG == 2 ? map_rank(&bar->acc_empty[0], 0) : su32(&bar->acc_empty[0]);
-        int n = 0;
-        bool ok = true;
-        for (int t = first; t < n_tiles && ok; t += step, ++n) {
-            int m0, n0;
-            tile_at(t, m0, n0);
-            m0 += rank * 128 + 32 * q;                    // this warp's 32 rows
-            const long long m = m0 + lane;
-            const bool live = m < p.M;
-            float rs = 1.f;
-            if constexpr (S8) rs = live ? p.row_scale[m] : 0.f;
-            ok = mbar_wait(&bar->acc_full[n & 1], (n >> 1) & 1);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + GT_N * (n & 1);
-            const bool rows_in = m0 < p.M;
-            if constexpr (EPI == EPI_STORE) {
-                if (p.out_dtype == MOE_FP32) {
-#pragma unroll 1
-                    for (int c = 0; c < GT_N; c += 32) {
-                        float v[32];
-                        load_acc<S8>(acc + c, v);
-                        if constexpr (S8) apply_scale(v, rs, p.col_scale0, n0 + c, p.N);
-                        if (S8 && p.bias)
+    }
+
+    const int q = warp & 3, team = (warp - GT_EPI_W0) >> 2;   // epilogue: lane quarter, which of its two warps
+    uint8_t *slot_buf = slots + (warp - GT_EPI_W0) * GT_SLOT;
+    // Columns [col, col + 32) of this lane's accumulator row: from TMEM, or summed over the splits of the cluster.
+    auto get = [&](uint32_t acc, int col, float (&v)[32]) {
+        uint32_t r[32];
+        if (p.splits == 1) {
+            tmem_ld32(acc + col, r);
+            tmem_wait();
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] += n0 + c + i < p.N ? __ldg(p.bias + n0 + c + i) : 0.f;
-                        stage32(ring.acquire(), lane, v);
-                        ring.release(&maps.out[0], n0 + c, m0, rows_in && n0 + c < p.N, p.add);
-                    }
-                } else {
-#pragma unroll 1
-                    for (int c = 0; c < GT_N; c += 64) {
-                        uint8_t *buf = ring.acquire();
+            for (int i = 0; i < 32; ++i) v[i] = acc_value<S8>(r[i]);
+        } else {
+            int sum[32] = {};
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float v[32];
-                            const int nc = n0 + c + 32 * h;
-                            load_acc<S8>(acc + c + 32 * h, v);
-                            if constexpr (S8) apply_scale(v, rs, p.col_scale0, nc, p.N);
-                            if (S8 && p.bias)
+            for (int i = 0; i < 32; ++i) v[i] = 0.f;
+            for (int j = 0; j < p.splits; ++j) {
+                const uint32_t src = map_rank(smem + (col * 128 + 32 * q + lane) * 4, j * CG + rank);
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) v[i] += nc + i < p.N ? __ldg(p.bias + nc + i) : 0.f;
-                            stage16(buf, lane, h, v, p.out_dtype == MOE_FP16);
-                        }
-                        ring.release(&maps.out[0], n0 + c, m0, rows_in && n0 + c < p.N);
-                    }
-                }
-            } else if constexpr (EPI == EPI_GATE) {
-                if constexpr (S8) {   // h in fp32, for the quantisation that follows
-#pragma unroll 1
-                    for (int c = 0; c < TN; c += 32) {
-                        float g[32], u[32];
-                        load_acc<S8>(acc + c, g);
-                        load_acc<S8>(acc + TN + c, u);
-                        apply_scale(g, rs, p.col_scale0, n0 + c, p.N);
-                        apply_scale(u, rs, p.col_scale1, n0 + c, p.N);
+                for (int i = 0; i < 32; ++i) r[i] = ld_cluster(src + i * 512);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) g[i] = act_fwd(p.act, g[i]) * u[i];
-                        stage32(ring.acquire(), lane, g);
-                        ring.release(&maps.out[0], n0 + c, m0, rows_in && n0 + c < p.N);
-                    }
-                } else {
-#pragma unroll 1
-                    for (int c = 0; c < TN; c += 64) {
-                        const bool in = rows_in && n0 + c < p.N;
-                        uint8_t *bg = ring.base, *bu = ring.base + GT_BUF, *bh = ring.base + 2 * GT_BUF;
-                        if (lane == 0) tma_wait_read<0>();
-                        __syncwarp();
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float g[32], u[32];
-                            load_acc<S8>(acc + c + 32 * h, g);
-                            load_acc<S8>(acc + TN + c + 32 * h, u);
-                            if (p.extra) {
-                                stage16(bg, lane, h, g, p.fp16);
-                                stage16(bu, lane, h, u, p.fp16);
-                            }
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) g[i] = act_fwd(p.act, g[i]) * u[i];
-                            stage16(bh, lane, h, g, p.fp16);
-                        }
-                        fence_async_smem();
-                        __syncwarp();
-                        if (lane == 0 && in) {
-                            tma_store(&maps.out[0], n0 + c, m0, bh);
-                            if (p.extra) {
-                                tma_store(&maps.out[1], n0 + c, m0, bg);
-                                tma_store(&maps.out[2], n0 + c, m0, bu);
-                            }
-                            tma_commit();
-                        }
-                    }
-                }
-            } else {
-                const uint16_t *gp = (const uint16_t *)p.in1 + m * p.N, *up = (const uint16_t *)p.in2 + m * p.N;
-#pragma unroll 1
-                for (int c = 0; c < TN; c += 64) {
-                    const bool in = rows_in && n0 + c < p.N;
-                    uint8_t *bg = ring.base, *bu = ring.base + GT_BUF, *bh = ring.base + 2 * GT_BUF;
-                    if (lane == 0) tma_wait_read<0>();
-                    __syncwarp();
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float v[32], du[32], hh[32];
-                        load_acc<S8>(acc + c + 32 * h, v);
-                        const int nc = n0 + c + 32 * h;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            uint4 gw = make_uint4(0, 0, 0, 0), uw = gw;
-                            if (live && nc + 8 * j < p.N) {   // N is a multiple of 8
-                                gw = *reinterpret_cast<const uint4 *>(gp + nc + 8 * j);
-                                uw = *reinterpret_cast<const uint4 *>(up + nc + 8 * j);
-                            }
-                            const uint32_t gs[4] = {gw.x, gw.y, gw.z, gw.w}, us[4] = {uw.x, uw.y, uw.z, uw.w};
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float2 z = unpack16(gs[i], p.fp16), u = unpack16(us[i], p.fp16);
-                                const int e = 8 * j + 2 * i;
-                                float a0, d0, a1, d1;
-                                act_bwd(p.act, z.x, a0, d0);
-                                act_bwd(p.act, z.y, a1, d1);
-                                du[e] = v[e] * a0, du[e + 1] = v[e + 1] * a1;
-                                hh[e] = a0 * u.x, hh[e + 1] = a1 * u.y;
-                                v[e] *= u.x * d0, v[e + 1] *= u.y * d1;
-                            }
-                        }
-                        stage16(bg, lane, h, v, p.fp16);
-                        stage16(bu, lane, h, du, p.fp16);
-                        if (p.extra) stage16(bh, lane, h, hh, p.fp16);
-                    }
-                    fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0 && in) {
-                        tma_store(&maps.out[0], n0 + c, m0, bg);
-                        tma_store(&maps.out[1], n0 + c, m0, bu);
-                        if (p.extra) tma_store(&maps.out[2], n0 + c, m0, bh);
-                        tma_commit();
-                    }
+                for (int i = 0; i < 32; ++i) {
+                    if constexpr (S8) sum[i] += (int)r[i];
+                    else v[i] += __uint_as_float(r[i]);
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(empty0 + 8 * (n & 1));   // the accumulator may be overwritten
+            if constexpr (S8)
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = (float)sum[i];
         }
-        if (lane == 0) tma_wait_all();
+    };
+    // Store tiles: three 16-bit ones in turn where a unit has one output, else all at once.
+    const bool rotate = (EPI == EPI_STORE && p.out_dtype != MOE_FP32) || (EPI == EPI_GATE && !S8 && !p.extra);
+    int turn = 0;
+    auto acquire = [&]() {
+        if (lane == 0) {
+            if (rotate) tma_wait_read<2>();
+            else tma_wait_read<0>();
+        }
         __syncwarp();
+        return slot_buf + 2048 * turn;
+    };
+    // One unit of 32 output columns: sub-tile `sub`, columns c.. of it.
+    auto unit = [&](uint32_t acc, int sub, int c, int m0, int n0, float rs) {
+        const int n = n0 + sub * (EPI == EPI_GATE ? half : W) + c;   // output column
+        const long long m = m0 + lane;
+        const bool in = m0 < p.M && n < p.N;
+        const int col = sub * GT_W + c;
+        float v[32];
+        uint8_t *buf;
+        if constexpr (EPI == EPI_STORE) {
+            get(acc, col, v);
+            if constexpr (S8) {
+                apply_scale(v, rs, p.col_scale0, n, p.N);
+                if (p.bias)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] += n + i < p.N ? __ldg(p.bias + n + i) : 0.f;
+            }
+            buf = acquire();
+            if (p.out_dtype == MOE_FP32) stage32(buf, lane, v);
+            else stage16(buf, lane, v, p.out_dtype == MOE_FP16);
+        } else if constexpr (EPI == EPI_GATE) {
+            float u[32];
+            get(acc, col, v);
+            get(acc, col + half, u);
+            if constexpr (S8) {
+                apply_scale(v, rs, p.col_scale0, n, p.N);
+                apply_scale(u, rs, p.col_scale1, n, p.N);
+            }
+            buf = acquire();
+            if constexpr (!S8)
+                if (p.extra) {
+                    stage16(buf + 2048, lane, v, p.fp16);
+                    stage16(buf + 4096, lane, u, p.fp16);
+                }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = act_fwd(p.act, v[i]) * u[i];
+            if constexpr (S8) stage32(buf, lane, v);   // h in fp32, for the quantisation that follows
+            else stage16(buf, lane, v, p.fp16);
+        } else {
+            const uint4 *gp = reinterpret_cast<const uint4 *>((const uint16_t *)p.in1 + m * p.N + n);
+            const uint4 *up = reinterpret_cast<const uint4 *>((const uint16_t *)p.in2 + m * p.N + n);
+            uint4 gw[4], uw[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                gw[j] = uw[j] = make_uint4(0, 0, 0, 0);
+                if (m < p.M && n + 8 * j < p.N) gw[j] = gp[j], uw[j] = up[j];   // N is a multiple of 8
+            }
+            get(acc, col, v);
+            buf = acquire();
+            float du[32], hh[32];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t gs[4] = {gw[j].x, gw[j].y, gw[j].z, gw[j].w}, us[4] = {uw[j].x, uw[j].y, uw[j].z, uw[j].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 z = unpack16(gs[i], p.fp16), u = unpack16(us[i], p.fp16);
+                    const int e = 8 * j + 2 * i;
+                    float a0, d0, a1, d1;
+                    act_bwd(p.act, z.x, a0, d0);
+                    act_bwd(p.act, z.y, a1, d1);
+                    du[e] = v[e] * a0, du[e + 1] = v[e + 1] * a1;
+                    hh[e] = a0 * u.x, hh[e + 1] = a1 * u.y;
+                    v[e] *= u.x * d0, v[e + 1] *= u.y * d1;
+                }
+            }
+            stage16(buf, lane, v, p.fp16);
+            stage16(buf + 2048, lane, du, p.fp16);
+            if (p.extra) stage16(buf + 4096, lane, hh, p.fp16);
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0 && in) {
+            if (EPI == EPI_STORE && p.add) tma_add(&maps.out[0], n, m0, buf);
+            else tma_store(&maps.out[0], n, m0, buf);
+            if (EPI == EPI_GATE_BWD || (EPI == EPI_GATE && !S8 && p.extra)) tma_store(&maps.out[1], n, m0, buf + 2048);
+            if (EPI != EPI_STORE && !S8 && p.extra) tma_store(&maps.out[2], n, m0, buf + 4096);
+            tma_commit();
+        }
+        if (rotate && in) turn = turn == 2 ? 0 : turn + 1;
+    };
+
+    const int sub_units = (EPI == EPI_GATE ? half : W) / GT_UNIT;
+    if (p.splits == 1) {
+        if (warp >= GT_EPI_W0) {
+            const uint32_t empty0 = CG == 2 ? map_rank(&bar->acc_empty[0], even) : su32(&bar->acc_empty[0]);
+            int n = 0;
+            for (int t = first; t < n_tiles; t += step, ++n) {
+                int m0, n0;
+                tile_at(t, m0, n0);
+                m0 += rank * 128 + 32 * q;                    // this warp's 32 rows
+                float rs = 1.f;
+                if constexpr (S8) rs = m0 + lane < p.M ? p.row_scale[m0 + lane] : 0.f;
+                const int slot = two_acc ? n & 1 : 0, use = two_acc ? n >> 1 : n;
+                if (!mbar_wait(&bar->acc_full[slot], use & 1)) break;
+                tc_fence_after();
+                const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + GT_W * slot;
+#pragma unroll 1
+                for (int u = team; u < sub_units * p.subs; u += 2)
+                    unit(acc, u / sub_units, GT_UNIT * (u % sub_units), m0, n0, rs);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(empty0 + 8 * slot);   // the accumulators may be overwritten
+            }
+        }
+    } else {
+        // one tile per cluster: every split leaves its accumulators in shared memory ([column][row], the ring is free
+        // once the last MMA has completed), and the splits share out the units
+        int m0, n0;
+        tile_at(first, m0, n0);
+        m0 += rank * 128 + 32 * q;
+        if (warp >= GT_EPI_W0 && mbar_wait(&bar->acc_full[0], 0)) {
+            tc_fence_after();
+            for (int c = 32 * team; c < W; c += 64) {
+                uint32_t r[32];
+                tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + c, r);
+                tmem_wait();
+                uint32_t *dst = reinterpret_cast<uint32_t *>(smem) + c * 128 + 32 * q + lane;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) dst[i * 128] = r[i];
+            }
+            tc_fence_before();
+        }
+        cluster_sync();
+        if (warp >= GT_EPI_W0) {
+            float rs = 1.f;
+            if constexpr (S8) rs = m0 + lane < p.M ? p.row_scale[m0 + lane] : 0.f;
+            for (int u = split + p.splits * team; u < sub_units; u += 2 * p.splits) unit(0, 0, GT_UNIT * u, m0, n0, rs);
+        }
     }
+    if (warp >= GT_EPI_W0 && lane == 0) tma_wait_all();
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if constexpr (CG == 2) cluster_sync();
+    if (CG * p.splits > 1) cluster_sync();
     tc_fence_after();
-    if (warp == 2) tmem_dealloc<CG>(tmem, 2 * GT_N);
-    if constexpr (CG == 2) cluster_sync();   // neither CTA leaves while the other still frees the pair's TMEM
+    if (warp == 2) tmem_dealloc<CG>(tmem, 2 * GT_W);
+    if (CG == 2) cluster_sync();   // neither CTA leaves while the other still frees the pair's TMEM
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
@@ -424,7 +441,8 @@ EncodeFn encoder() {
     return fn;
 }
 
-// Tiles of box_inner x box_outer elements of a row-major [outer][inner] matrix, 128-byte swizzle.
+// Tiles of box_inner x box_outer elements of a row-major [outer][inner] matrix, swizzled over the tile row's 64 or 128
+// bytes.
 int encode(CUtensorMap *m, int dtype, const void *p, long long inner, long long outer, long long ld, int box_inner, int box_outer) {
     EncodeFn fn = encoder();
     if (!fn) return set_error(MOE_ERR_CUDA, "cuTensorMapEncodeTiled is not available in this driver");
@@ -435,53 +453,119 @@ int encode(CUtensorMap *m, int dtype, const void *p, long long inner, long long 
     const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer}, strides[1] = {(cuuint64_t)ld * size};
     const cuuint32_t box[2] = {(cuuint32_t)box_inner, (cuuint32_t)box_outer}, es[2] = {1, 1};
     const CUresult r = fn(m, t, 2, const_cast<void *>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                          box_inner * size == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? MOE_OK : set_error(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed");
 }
 
+constexpr int kMaxDevices = 64;
+
+int current_device(int *dev) {
+    QE_CHECK(cudaGetDevice(dev));
+    return *dev < kMaxDevices ? MOE_OK : set_error(MOE_ERR_UNSUPPORTED, "device index above 63");
+}
+
 template <bool S8, bool A_MN, bool B_MN, int EPI, int CG>
-int launch_tc(const Maps &maps, const TileArgs &p, cudaStream_t st) {
+int launch_tc(const Maps &maps, const TileArgs &p, int clusters, cudaStream_t st) {
     auto kern = k_gemm_tc<S8, A_MN, B_MN, EPI, CG>;
-    constexpr int kMaxDevices = 64;
-    static int units[kMaxDevices] = {};   // tiles in flight on a device: looked up once, racing threads store the same
+    static int ready[kMaxDevices] = {};   // this kernel's shared-memory limit is set on the device
     int dev = 0;
-    QE_CHECK(cudaGetDevice(&dev));
-    if (dev >= kMaxDevices) return set_error(MOE_ERR_UNSUPPORTED, "device index above 63");
+    QE_TRY(current_device(&dev));
+    if (!__atomic_load_n(&ready[dev], __ATOMIC_RELAXED)) {
+        QE_CHECK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GT_SMEM));
+        __atomic_store_n(&ready[dev], 1, __ATOMIC_RELAXED);
+    }
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[1];
+    cfg.gridDim = dim3(clusters * CG * p.splits);
     cfg.blockDim = dim3(GT_NT);
     cfg.dynamicSmemBytes = GT_SMEM;
     cfg.stream = st;
     cfg.attrs = at;
     cfg.numAttrs = 1;
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim = {CG, 1, 1};
-    int n = __atomic_load_n(&units[dev], __ATOMIC_RELAXED);
-    if (n == 0) {
-        int sms = 0;
-        QE_CHECK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GT_SMEM));
-        QE_CHECK(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-        cfg.gridDim = dim3(sms / CG * CG);
-        QE_CHECK(cudaOccupancyMaxActiveClusters(&n, kern, &cfg));
-        if (n < 1) return set_error(MOE_ERR_UNSUPPORTED, "the device cannot hold the product's kernel");
-        __atomic_store_n(&units[dev], n, __ATOMIC_RELAXED);
-    }
-    cfg.gridDim = dim3(std::min(n, p.tiles_m * p.tiles_n) * CG);
+    at[0].val.clusterDim = {(unsigned)(CG * p.splits), 1, 1};
     QE_CHECK(cudaLaunchKernelEx(&cfg, kern, maps, p));
     QE_CHECK_LAUNCH("k_gemm_tc");
     return MOE_OK;
 }
 
+// Clusters of `size` CTAs that the current device runs at once (looked up once per device and size; racing threads
+// store the same number).
+int active_clusters(int size, int *out) {
+    static int known[kMaxDevices][9] = {};
+    int dev = 0;
+    QE_TRY(current_device(&dev));
+    int n = __atomic_load_n(&known[dev][size], __ATOMIC_RELAXED);
+    if (n == 0) {
+        auto kern = k_gemm_tc<false, false, false, EPI_STORE, 1>;   // every variant has this kernel's needs
+        QE_CHECK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GT_SMEM));
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute at[1];
+        cfg.gridDim = dim3(size * 1024);
+        cfg.blockDim = dim3(GT_NT);
+        cfg.dynamicSmemBytes = GT_SMEM;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim = {(unsigned)size, 1, 1};
+        QE_CHECK(cudaOccupancyMaxActiveClusters(&n, kern, &cfg));
+        if (n < 1) return set_error(MOE_ERR_UNSUPPORTED, "the device cannot hold the product's kernel");
+        __atomic_store_n(&known[dev][size], n, __ATOMIC_RELAXED);
+    }
+    *out = n;
+    return MOE_OK;
+}
+
+struct Shape {
+    int cg, W, subs, splits;
+};
+
+// The tile shape with the least modelled time, in SM cycles.  A k step takes the longer of its MMAs (2 cycles a column:
+// 128 rows x 64 values x 1 column at 4096 multiply-adds a cycle) and its loads (64 bytes a cycle from L2 to an SM); a
+// tile's epilogue about 24 cycles a column (measured between 15 for plain stores and 40 for the gate's gradient); a
+// launch about 6000 cycles of start and end.
+int choose(const GemmArgs &g, int ksteps, Shape *best) {
+    long long least = -1;
+    for (int cg = g.M > 128 ? 2 : 1; cg >= 1; --cg) {
+        const int tiles_m = (g.M + 128 * cg - 1) / (128 * cg);
+        for (int splits = 1; splits <= 8 / cg && splits <= ksteps / 4 + 1; splits = splits < 4 ? splits + 1 : 2 * splits) {
+            if ((splits - 1) * ((ksteps + splits - 1) / splits) >= ksteps) continue;   // no split without a k step
+            int room = 0;
+            QE_TRY(active_clusters(cg * splits, &room));
+            for (int subs = 1; subs <= (splits == 1 ? 2 : 1); ++subs) {
+                // sub-tile widths: halves of whole 32-column units (gate), of 64 rows where B has its row index contiguous
+                const int unit = g.b_mn ? 128 : g.epi == EPI_GATE ? 64 : 32;
+                for (int W = subs == 2 ? 128 + unit : unit; W <= GT_W; W += unit) {
+                    const int C = W * subs, out = g.epi == EPI_GATE ? C / 2 : C;
+                    const long long tiles = (long long)tiles_m * ((g.N + out - 1) / out);
+                    const long long waves = (tiles + room - 1) / room;
+                    if (subs == 2 && waves > 1) continue;
+                    const long long step = std::max(2 * C, (GT_A + C * 128 / cg) / 64);
+                    const long long main = (long long)((ksteps + splits - 1) / splits) * step, epi = 24 * C;
+                    long long t = 6000;
+                    if (splits > 1) t += waves * (main + 3000 + 12 * C + epi / splits);
+                    else t += (waves - 1) * std::max(main, epi) + main + epi;
+                    if (least < 0 || t < least) {
+                        least = t;
+                        *best = {cg, W, subs, splits};
+                    }
+                }
+            }
+        }
+    }
+    return MOE_OK;
+}
+
 template <int CG>
-int dispatch(const GemmArgs &g, const Maps &m, const TileArgs &p, cudaStream_t st) {
+int dispatch(const GemmArgs &g, const Maps &m, const TileArgs &p, int clusters, cudaStream_t st) {
     if (g.type == DT_S8)
-        return g.epi == EPI_GATE ? launch_tc<true, false, false, EPI_GATE, CG>(m, p, st)
-                                 : launch_tc<true, false, false, EPI_STORE, CG>(m, p, st);
-    if (g.epi == EPI_GATE) return launch_tc<false, false, false, EPI_GATE, CG>(m, p, st);
-    if (g.epi == EPI_GATE_BWD) return launch_tc<false, false, true, EPI_GATE_BWD, CG>(m, p, st);
-    if (g.a_mn) return launch_tc<false, true, true, EPI_STORE, CG>(m, p, st);
-    if (g.b_mn) return launch_tc<false, false, true, EPI_STORE, CG>(m, p, st);
-    return launch_tc<false, false, false, EPI_STORE, CG>(m, p, st);
+        return g.epi == EPI_GATE ? launch_tc<true, false, false, EPI_GATE, CG>(m, p, clusters, st)
+                                 : launch_tc<true, false, false, EPI_STORE, CG>(m, p, clusters, st);
+    if (g.epi == EPI_GATE) return launch_tc<false, false, false, EPI_GATE, CG>(m, p, clusters, st);
+    if (g.epi == EPI_GATE_BWD) return launch_tc<false, false, true, EPI_GATE_BWD, CG>(m, p, clusters, st);
+    if (g.a_mn) return launch_tc<false, true, true, EPI_STORE, CG>(m, p, clusters, st);
+    if (g.b_mn) return launch_tc<false, false, true, EPI_STORE, CG>(m, p, clusters, st);
+    return launch_tc<false, false, false, EPI_STORE, CG>(m, p, clusters, st);
 }
 
 }  // namespace
@@ -496,14 +580,20 @@ int read_dense_error(int *code) {
 int launch_gemm(const GemmArgs &g, Link link, cudaStream_t st) {
     if (g.M <= kFewRows && !g.a_mn && !g.b_mn && g.segs == 1) return launch_rows(g, link, st);
     const int bk = g.type == DT_S8 ? 128 : 64;
-    const int cg = g.M > 128 ? 2 : 1;
     Maps m;
     TileArgs p = {};
     p.M = g.M, p.N = g.N, p.segs = g.segs;
     p.kblocks = (g.K + bk - 1) / bk;
-    const int tm = 128 * cg, tn = g.epi == EPI_GATE ? GT_N / 2 : GT_N;
+    Shape sh = {};
+    QE_TRY(choose(g, p.kblocks * g.segs, &sh));
+    const int cg = sh.cg, tm = 128 * cg, half = sh.W / 2;
+    const int tn = (g.epi == EPI_GATE ? half : sh.W) * sh.subs;
     p.tiles_m = (g.M + tm - 1) / tm;
     p.tiles_n = (g.N + tn - 1) / tn;
+    p.W = sh.W, p.subs = sh.subs, p.splits = sh.splits;
+    p.kper = (p.kblocks * g.segs + sh.splits - 1) / sh.splits;
+    p.stage_bytes = GT_A + sh.W * sh.subs / cg * 128;
+    p.stages = std::min(GT_MAX_STAGES, GT_RING / p.stage_bytes);
     p.act = g.act;
     p.fp16 = g.type == MOE_FP16;
     p.out_dtype = g.out_dtype;
@@ -511,20 +601,25 @@ int launch_gemm(const GemmArgs &g, Link link, cudaStream_t st) {
     p.extra = g.out2 != nullptr;
     p.in1 = g.in1, p.in2 = g.in2;
     p.row_scale = g.row_scale, p.col_scale0 = g.col_scale[0], p.col_scale1 = g.col_scale[1], p.bias = g.bias;
-    for (int s = 0; s < 2; ++s) {
-        const void *a = g.a[s] ? g.a[s] : g.a[0], *b = g.b[s] ? g.b[s] : g.b[0];
-        if (g.a_mn) QE_TRY(encode(&m.a[s], g.type, a, g.M, g.K, g.lda, 64, bk));
-        else QE_TRY(encode(&m.a[s], g.type, a, g.K, g.M, g.lda, bk, 128));
-        if (g.b_mn) QE_TRY(encode(&m.b[s], g.type, b, g.N, g.K, g.ldb, 64, bk));
-        else QE_TRY(encode(&m.b[s], g.type, b, g.K, g.N, g.ldb, bk, 128));
+    const int na = g.segs, nb = g.epi == EPI_GATE ? 2 : g.segs;
+    for (int s = 0; s < na; ++s) {
+        if (g.a_mn) QE_TRY(encode(&m.a[s], g.type, g.a[s], g.M, g.K, g.lda, 64, bk));
+        else QE_TRY(encode(&m.a[s], g.type, g.a[s], g.K, g.M, g.lda, bk, 128));
     }
-    void *outs[3] = {g.out, g.out1 ? g.out1 : g.out, g.out2 ? g.out2 : g.out};
-    for (int i = 0; i < 3; ++i) {
-        const bool main = outs[i] == g.out;
-        const int t = main ? g.out_dtype : g.type;
-        QE_TRY(encode(&m.out[i], t, outs[i], g.N, g.M, main ? g.ldo : g.N, t == MOE_FP32 ? 32 : 64, 32));
+    for (int s = 0; s < nb; ++s) {
+        if (g.b_mn) QE_TRY(encode(&m.b[s], g.type, g.b[s], g.N, g.K, g.ldb, 64, bk));
+        else QE_TRY(encode(&m.b[s], g.type, g.b[s], g.K, g.N, g.ldb, bk, half));
     }
-    return cg == 2 ? dispatch<2>(g, m, p, st) : dispatch<1>(g, m, p, st);
+    QE_TRY(encode(&m.out[0], g.out_dtype, g.out, g.N, g.M, g.ldo, GT_UNIT, 32));
+    if (g.out1) QE_TRY(encode(&m.out[1], g.type, g.out1, g.N, g.M, g.N, GT_UNIT, 32));
+    if (g.out2) QE_TRY(encode(&m.out[2], g.type, g.out2, g.N, g.M, g.N, GT_UNIT, 32));
+    const int tiles = p.tiles_m * p.tiles_n;
+    int clusters = tiles;
+    if (p.splits == 1) {
+        QE_TRY(active_clusters(cg, &clusters));
+        clusters = std::min(clusters, tiles);
+    }
+    return cg == 2 ? dispatch<2>(g, m, p, clusters, st) : dispatch<1>(g, m, p, clusters, st);
 }
 
 }  // namespace qeffn

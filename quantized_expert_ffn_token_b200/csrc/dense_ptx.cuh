@@ -60,6 +60,12 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// A float of another CTA's shared memory.
+__device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -138,11 +144,12 @@ __device__ __forceinline__ void umma(uint32_t d, uint64_t a, uint64_t b, uint32_
         asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
                      "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
 }
-// Arrive on *b (in a pair: on the same barrier of both CTAs) once every MMA this thread issued has completed.
+// Arrive on *b (in a pair: on the same barrier of both CTAs, cluster ranks `even` and even + 1) once every MMA this
+// thread issued has completed.
 template <int CG>
-__device__ __forceinline__ void umma_commit(uint64_t *b) {
+__device__ __forceinline__ void umma_commit(uint64_t *b, uint32_t even) {
     if constexpr (CG == 2) {
-        const uint16_t both = 3;
+        const uint16_t both = (uint16_t)(3u << even);
         asm volatile(
             "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(su32(b)),
             "h"(both) : "memory");
