@@ -105,6 +105,37 @@ __device__ __forceinline__ void apply_scale(float (&v)[32], float rs, const floa
     for (int i = 0; i < 32; ++i) v[i] *= rs * (n + i < N ? __ldg(cs + n + i) : 0.f);
 }
 
+// g = act(g) u for a unit; the choice of the activation stays outside the unrolled loops (inside, the code of all three
+// for 32 elements did not fit the instruction cache: 4.6 us for one tile's epilogue).
+template <int ACT>
+__device__ __forceinline__ void gate_as(float (&g)[32], const float (&u)[32]) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) g[i] = act_fwd(ACT, g[i]) * u[i];
+}
+__device__ __forceinline__ void gate_all(int act, float (&g)[32], const float (&u)[32]) {
+    if (act == MOE_ACT_SILU) gate_as<MOE_ACT_SILU>(g, u);
+    else if (act == MOE_ACT_GELU_TANH) gate_as<MOE_ACT_GELU_TANH>(g, u);
+    else gate_as<MOE_ACT_GELU>(g, u);
+}
+// In: v = dh, u = up, g = gate.  Out: v = dg, u = du, g = h.
+template <int ACT>
+__device__ __forceinline__ void gate_bwd_as(float (&v)[32], float (&u)[32], float (&g)[32]) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        float a, d;
+        act_bwd(ACT, g[i], a, d);
+        const float dh = v[i], up = u[i];
+        v[i] = dh * up * d;
+        u[i] = dh * a;
+        g[i] = a * up;
+    }
+}
+__device__ __forceinline__ void gate_bwd_all(int act, float (&v)[32], float (&u)[32], float (&g)[32]) {
+    if (act == MOE_ACT_SILU) gate_bwd_as<MOE_ACT_SILU>(v, u, g);
+    else if (act == MOE_ACT_GELU_TANH) gate_bwd_as<MOE_ACT_GELU_TANH>(v, u, g);
+    else gate_bwd_as<MOE_ACT_GELU>(v, u, g);
+}
+
 template <bool S8, bool A_MN, bool B_MN, int EPI, int CG>
 __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Maps maps, const __grid_constant__ TileArgs p) {
     constexpr int BK = S8 ? 128 : 64;             // reduction values per stage
@@ -113,7 +144,7 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
     uint8_t *smem = smem_raw + ((1024 - (su32(smem_raw) & 1023)) & 1023);
     uint8_t *slots = smem + GT_RING;
     GtBars *bar = reinterpret_cast<GtBars *>(slots + GT_EPI_NW * GT_SLOT);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // warp: uniform
     const uint32_t crank = cluster_rank();
     const uint32_t rank = CG == 2 ? crank & 1 : 0, even = crank - rank;   // rank in the pair, the pair's first CTA
     const int split = crank / CG;
@@ -152,19 +183,19 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
     };
 
     if (warp == 0) {
-        if (lane == 0) {
-            int s = 0, filled = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            for (int t = first; t < n_tiles && ok; t += step) {
-                int m0, n0;
-                tile_at(t, m0, n0);
-                m0 += rank * 128;
-                for (int kb = k_begin; kb < k_end; ++kb) {
-                    ok = mbar_wait(&bar->empty[s], phase ^ 1);
-                    if (!ok) break;
-                    const int seg = kb >= p.kblocks, k0 = (kb - seg * p.kblocks) * BK;
-                    uint8_t *sa = smem + s * p.stage_bytes, *sb = sa + GT_A;
+        int s = 0, filled = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int t = first; t < n_tiles && ok; t += step) {
+            int m0, n0;
+            tile_at(t, m0, n0);
+            m0 += rank * 128;
+            for (int kb = k_begin; kb < k_end; ++kb) {
+                ok = mbar_wait(&bar->empty[s], phase ^ 1);
+                if (!ok) break;
+                const int seg = kb >= p.kblocks, k0 = (kb - seg * p.kblocks) * BK;
+                uint8_t *sa = smem + s * p.stage_bytes, *sb = sa + GT_A;
+                if (elect_one()) {
                     if (rank == 0) mbar_expect_tx(&bar->full[s], CG * p.stage_bytes);
                     const uint32_t fb = CG == 2 ? map_rank(&bar->full[s], even) : su32(&bar->full[s]);
                     const CUtensorMap *ma = &maps.a[seg];
@@ -192,40 +223,41 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
                         load_b(0, 1);
                         if (p.subs == 2) load_b(1, 0), load_b(1, 1);
                     }
-                    ++filled;
-                    if (++s == p.stages) s = 0, phase ^= 1;
                 }
+                __syncwarp();
+                ++filled;
+                if (++s == p.stages) s = 0, phase ^= 1;
             }
-            // every copy has landed before the CTAs leave: the last fills that no MMA waited for
-            if (!ok && rank == 0)
-                for (int j = 0; j < p.stages && j < filled; ++j) {
-                    if (s == 0) s = p.stages, phase ^= 1;
-                    --s;
-                    mbar_wait(&bar->full[s], phase, true);
-                }
         }
+        // every copy has landed before the CTAs leave: the last fills that no MMA waited for
+        if (!ok && rank == 0)
+            for (int j = 0; j < p.stages && j < filled; ++j) {
+                if (s == 0) s = p.stages, phase ^= 1;
+                --s;
+                mbar_wait(&bar->full[s], phase, true);
+            }
         __syncwarp();
-    } else if (warp == 1) {
-        if (rank == 0 && lane == 0) {
-            const uint32_t idesc = (S8 ? (2u << 4) | (1u << 7) | (1u << 10)
-                                       : (1u << 4) | (p.fp16 ? 0u : (1u << 7) | (1u << 10))) |
-                                   (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u) | ((uint32_t)(W >> 3) << 17) |
-                                   ((uint32_t)(TM >> 4) << 24);
-            int s = 0, n = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            for (int t = first; t < n_tiles && ok; t += step, ++n) {
-                const int slot = two_acc ? n & 1 : 0, use = two_acc ? n >> 1 : n;
-                ok = mbar_wait(&bar->acc_empty[slot], (use & 1) ^ 1);
+    } else if (warp == 1 && rank == 0) {
+        const uint32_t idesc = (S8 ? (2u << 4) | (1u << 7) | (1u << 10)
+                                   : (1u << 4) | (p.fp16 ? 0u : (1u << 7) | (1u << 10))) |
+                               (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u) | ((uint32_t)(W >> 3) << 17) |
+                               ((uint32_t)(TM >> 4) << 24);
+        int s = 0, n = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int t = first; t < n_tiles && ok; t += step, ++n) {
+            const int slot = two_acc ? n & 1 : 0, use = two_acc ? n >> 1 : n;
+            ok = mbar_wait(&bar->acc_empty[slot], (use & 1) ^ 1);
+            if (!ok) break;
+            tc_fence_after();
+            for (int kb = k_begin; kb < k_end; ++kb) {
+                ok = mbar_wait(&bar->full[s], phase);
                 if (!ok) break;
                 tc_fence_after();
-                for (int kb = k_begin; kb < k_end; ++kb) {
-                    ok = mbar_wait(&bar->full[s], phase);
-                    if (!ok) break;
-                    tc_fence_after();
-                    // 32 bytes of k at a time: within the 128-byte rows, or 16 of the 128-byte rows
-                    const uint32_t a0 = su32(smem + s * p.stage_bytes), acc = tmem + GT_W * slot;
-                    const uint64_t ad = smem_desc(a0, A_MN ? 64 * 128 : 16), bd = smem_desc(a0 + GT_A, B_MN ? 64 * 128 : 16);
+                // 32 bytes of k at a time: within the 128-byte rows, or 16 of the 128-byte rows
+                const uint32_t a0 = su32(smem + s * p.stage_bytes), acc = tmem + GT_W * slot;
+                const uint64_t ad = smem_desc(a0, A_MN ? 64 * 128 : 16), bd = smem_desc(a0 + GT_A, B_MN ? 64 * 128 : 16);
+                if (elect_one()) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         umma<S8, CG>(acc, ad + (A_MN ? 128 : 2) * j, bd + (B_MN ? 128 : 2) * j, idesc, kb > k_begin || j > 0);
@@ -236,14 +268,16 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
                             umma<S8, CG>(acc + GT_W, ad + (A_MN ? 128 : 2) * j, b1 + (B_MN ? 128 : 2) * j, idesc, kb > k_begin || j > 0);
                     }
                     umma_commit<CG>(&bar->empty[s], even);
-                    if (++s == p.stages) s = 0, phase ^= 1;
                 }
-                if (ok) umma_commit<CG>(&bar->acc_full[slot], even);
+                __syncwarp();
+                if (++s == p.stages) s = 0, phase ^= 1;
             }
-            umma_commit<CG>(&bar->mma_done, even);   // no MMA may still use shared memory or TMEM when the CTAs leave
-            mbar_wait(&bar->mma_done, 0, true);
+            if (ok && elect_one()) umma_commit<CG>(&bar->acc_full[slot], even);
+            __syncwarp();
         }
+        if (elect_one()) umma_commit<CG>(&bar->mma_done, even);   // no MMA may still use shared memory or TMEM when the CTAs leave
         __syncwarp();
+        mbar_wait(&bar->mma_done, 0, true);
     }
 
     const int q = warp & 3, team = (warp - GT_EPI_W0) >> 2;   // epilogue: lane quarter, which of its two warps
@@ -319,8 +353,7 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
                     stage16(buf + 2048, lane, v, p.fp16);
                     stage16(buf + 4096, lane, u, p.fp16);
                 }
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = act_fwd(p.act, v[i]) * u[i];
+            gate_all(p.act, v, u);
             if constexpr (S8) stage32(buf, lane, v);   // h in fp32, for the quantisation that follows
             else stage16(buf, lane, v, p.fp16);
         } else {
@@ -342,14 +375,10 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
                 for (int i = 0; i < 4; ++i) {
                     const float2 z = unpack16(gs[i], p.fp16), u = unpack16(us[i], p.fp16);
                     const int e = 8 * j + 2 * i;
-                    float a0, d0, a1, d1;
-                    act_bwd(p.act, z.x, a0, d0);
-                    act_bwd(p.act, z.y, a1, d1);
-                    du[e] = v[e] * a0, du[e + 1] = v[e + 1] * a1;
-                    hh[e] = a0 * u.x, hh[e + 1] = a1 * u.y;
-                    v[e] *= u.x * d0, v[e + 1] *= u.y * d1;
+                    hh[e] = z.x, hh[e + 1] = z.y, du[e] = u.x, du[e + 1] = u.y;
                 }
             }
+            gate_bwd_all(p.act, v, du, hh);
             stage16(buf, lane, v, p.fp16);
             stage16(buf + 2048, lane, du, p.fp16);
             if (p.extra) stage16(buf + 4096, lane, hh, p.fp16);
@@ -577,15 +606,12 @@ int read_dense_error(int *code) {
     return MOE_OK;
 }
 
-int launch_gemm(const GemmArgs &g, Link link, cudaStream_t st) {
-    if (g.M <= kFewRows && !g.a_mn && !g.b_mn && g.segs == 1) return launch_rows(g, link, st);
+static int launch_shape(const GemmArgs &g, const Shape &sh, cudaStream_t st) {
     const int bk = g.type == DT_S8 ? 128 : 64;
     Maps m;
     TileArgs p = {};
     p.M = g.M, p.N = g.N, p.segs = g.segs;
     p.kblocks = (g.K + bk - 1) / bk;
-    Shape sh = {};
-    QE_TRY(choose(g, p.kblocks * g.segs, &sh));
     const int cg = sh.cg, tm = 128 * cg, half = sh.W / 2;
     const int tn = (g.epi == EPI_GATE ? half : sh.W) * sh.subs;
     p.tiles_m = (g.M + tm - 1) / tm;
@@ -620,6 +646,14 @@ int launch_gemm(const GemmArgs &g, Link link, cudaStream_t st) {
         clusters = std::min(clusters, tiles);
     }
     return cg == 2 ? dispatch<2>(g, m, p, clusters, st) : dispatch<1>(g, m, p, clusters, st);
+}
+
+int launch_gemm(const GemmArgs &g, Link link, cudaStream_t st) {
+    if (g.M <= kFewRows && !g.a_mn && !g.b_mn && g.segs == 1) return launch_rows(g, link, st);
+    const int bk = g.type == DT_S8 ? 128 : 64;
+    Shape sh = {};
+    QE_TRY(choose(g, (g.K + bk - 1) / bk * g.segs, &sh));
+    return launch_shape(g, sh, st);
 }
 
 }  // namespace qeffn
