@@ -44,12 +44,13 @@ struct GemmArgs {
     bool add = false;             // EPI_STORE with fp32 out: out += C
 };
 
-// Position of a kernel in its call.  The streaming and quantising kernels let the next kernel start early (programmatic
-// launch), after their own wait for the one before; so when a later kernel of a call runs, everything before the call
-// is complete, and it may load the call's weights before it waits for the call's intermediate results.  A call's first
-// kernel reads nothing before its wait, because the kernel before it may be the one that writes its inputs.
+// Position of a product in its call.  Every kernel here is launched programmatically: it starts while the kernel before
+// it drains, waits for that one's results before it touches them, and only then lets the next kernel start; so when a
+// later kernel of a call runs, everything before the call is complete.  A call's first kernel reads nothing before its
+// wait, because the kernel before it may be the one that writes its inputs; a later one may load operands that are
+// inputs of the call.
 struct Link {
-    bool first = true;
+    bool b_ready = false;   // a later kernel of the call, and B is an input of the call
 };
 constexpr int kFewRows = 32;   // products of at most this many rows stream the weights (dense_rows.cu)
 int launch_gemm(const GemmArgs &g, Link link, cudaStream_t st);

@@ -159,7 +159,7 @@ int moe_ffn_forward(const moe_ffn *f, const void *x, long long ld_x, int T, void
     g.b[0] = f->w_gate, g.b[1] = f->w_up, g.ldb = d;
     g.epi = EPI_GATE, g.act = f->act;
     g.out = w.h, g.out_dtype = f->dtype, g.ldo = I, g.out1 = gate, g.out2 = up;
-    QE_TRY(launch_gemm(g, {true}, st));
+    QE_TRY(launch_gemm(g, {}, st));
 
     GemmArgs y2;
     y2.type = f->dtype;
@@ -167,7 +167,7 @@ int moe_ffn_forward(const moe_ffn *f, const void *x, long long ld_x, int T, void
     y2.a[0] = w.h, y2.lda = I;
     y2.b[0] = f->w_down, y2.ldb = I;
     y2.out = y, y2.out_dtype = f->dtype, y2.ldo = ly;
-    return launch_gemm(y2, {false}, st);
+    return launch_gemm(y2, {true}, st);
 }
 
 int moe_ffn_backward(const moe_ffn *f, const void *x, long long ld_x, const void *gate, const void *up, const void *dy,
@@ -220,7 +220,7 @@ int moe_ffn_backward(const moe_ffn *f, const void *x, long long ld_x, const void
         p.a[0] = w.dg, p.a[1] = w.du, p.lda = I;
         p.b[0] = f->w_gate, p.b[1] = f->w_up, p.ldb = d, p.b_mn = true;
         p.out = dx, p.out_dtype = f->dtype, p.ldo = ldx;
-        QE_TRY(launch_gemm(p, {}, st));
+        QE_TRY(launch_gemm(p, {true}, st));
     }
     if (dw) {
         GemmArgs p;
@@ -232,9 +232,9 @@ int moe_ffn_backward(const moe_ffn *f, const void *x, long long ld_x, const void
         p.M = I, p.N = d, p.lda = I, p.ldb = lx, p.ldo = d;
         p.b[0] = x;
         p.a[0] = w.dg, p.out = dw_gate;
-        QE_TRY(launch_gemm(p, {}, st));
+        QE_TRY(launch_gemm(p, {true}, st));
         p.a[0] = w.du, p.out = dw_up;
-        QE_TRY(launch_gemm(p, {}, st));
+        QE_TRY(launch_gemm(p, {true}, st));
         p.M = d, p.N = I, p.lda = ldy, p.ldb = I, p.ldo = I;
         p.a[0] = dy, p.b[0] = w.h, p.out = dw_down;
         QE_TRY(launch_gemm(p, {}, st));
@@ -323,7 +323,7 @@ int moe_ffn_s8_forward(const moe_ffn_s8 *f, const void *x, long long ld_x, int T
     g.row_scale = w.xs, g.col_scale[0] = f->s_gate, g.col_scale[1] = f->s_up;
     g.epi = EPI_GATE, g.act = f->act;
     g.out = w.h, g.out_dtype = MOE_FP32, g.ldo = I;
-    QE_TRY(launch_gemm(g, {false}, st));
+    QE_TRY(launch_gemm(g, {true}, st));
     QE_TRY(launch_quantize_s8(w.h, MOE_FP32, I, T, I, w.hq, w.hs, st));
     GemmArgs p;
     p.type = DT_S8;
@@ -331,7 +331,7 @@ int moe_ffn_s8_forward(const moe_ffn_s8 *f, const void *x, long long ld_x, int T
     p.a[0] = w.hq, p.lda = I, p.b[0] = f->w_down, p.ldb = I;
     p.row_scale = w.hs, p.col_scale[0] = f->s_down;
     p.out = y, p.out_dtype = f->dtype, p.ldo = ly;
-    return launch_gemm(p, {false}, st);
+    return launch_gemm(p, {true}, st);
 }
 
 int moe_ffn_get_device_error(int *code) {

@@ -33,7 +33,8 @@ namespace {
 
 constexpr int GT_NT = 384;
 constexpr int GT_W = 256;                   // largest sub-tile width; TMEM columns between accumulators
-constexpr int GT_A = 128 * 128;             // bytes of A per stage: 128 rows of one k step
+constexpr int GT_KB = 128;                  // bytes of the reduction index per stage
+constexpr int GT_A = 128 * GT_KB;           // bytes of A per stage: 128 rows of one k step
 constexpr int GT_MAX_STAGES = 8;
 constexpr int GT_RING = 177 * 1024;         // bytes of the stage ring
 constexpr int GT_EPI_W0 = 4, GT_EPI_NW = 8;
@@ -51,6 +52,8 @@ struct TileArgs {
     int W, subs;                // sub-tile width, sub-tiles per tile
     int splits, kper;           // reduction splits (CTAs or pairs of a cluster), k steps each
     int stages, stage_bytes;
+    int a_rows;                 // rows of an A box: fewer than 128 where all rows fit in one
+    int b_ready;                // B does not depend on kernels of the same call: it may be loaded before the wait
     int act;
     int fp16;                   // 16-bit operands (and out1, out2): fp16 rather than bf16
     int out_dtype;
@@ -170,6 +173,12 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
     if (CG * p.splits > 1) cluster_sync();
     tc_fence_after();
     const uint32_t tmem = bar->tmem;
+    // programmatic launch: all of the above overlapped the kernel before; its results are touched from here on (the
+    // producer of a product whose B is an input of the call first fills the ring with B)
+    if (!(warp == 0 && p.b_ready)) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        asm volatile("griddepcontrol.launch_dependents;");
+    }
 
     const int n_tiles = p.tiles_m * p.tiles_n;
     const int first = blockIdx.x / (CG * p.splits), step = gridDim.x / (CG * p.splits);
@@ -186,6 +195,54 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
         int s = 0, filled = 0;
         uint32_t phase = 0;
         bool ok = true;
+        const uint32_t a_bytes = A_MN ? GT_A : p.a_rows * GT_KB;
+        // copies of k step kb of tile (m0, n0) into stage s: A's and B's (by the elected lane)
+        auto load_a = [&](int st, int kb, int m0) {
+            const int seg = kb >= p.kblocks, k0 = (kb - seg * p.kblocks) * BK;
+            uint8_t *sa = smem + st * p.stage_bytes;
+            const uint32_t fb = CG == 2 ? map_rank(&bar->full[st], even) : su32(&bar->full[st]);
+            if constexpr (A_MN) {
+                tma_load<CG>(sa, &maps.a[seg], m0, k0, fb);
+                tma_load<CG>(sa + GT_A / 2, &maps.a[seg], m0 + 64, k0, fb);
+            } else {
+                tma_load<CG>(sa, &maps.a[seg], k0, m0, fb);
+            }
+        };
+        auto load_b = [&](int st, int kb, int n0) {
+            const int seg = kb >= p.kblocks, k0 = (kb - seg * p.kblocks) * BK;
+            uint8_t *sb = smem + st * p.stage_bytes + GT_A;
+            const uint32_t fb = CG == 2 ? map_rank(&bar->full[st], even) : su32(&bar->full[st]);
+            if (rank == 0) mbar_expect_tx(&bar->full[st], CG * (p.stage_bytes - GT_A + a_bytes));
+            auto rows = [&](int sub, int h) {   // half h of a sub-tile's rows
+                const CUtensorMap *mb = EPI == EPI_GATE ? &maps.b[h] : &maps.b[seg];
+                const int nb = EPI == EPI_GATE ? n0 + sub * half : n0 + sub * W + h * half;
+                if constexpr (B_MN) {
+                    for (int c = 0; c < half; c += 64, sb += 64 * 128) tma_load<CG>(sb, mb, nb + c, k0, fb);
+                } else {
+                    tma_load<CG>(sb, mb, k0, nb, fb);
+                    sb += half * 128;
+                }
+            };
+            if constexpr (CG == 2) {
+                rows(0, rank);
+                if (p.subs == 2) rows(1, rank);
+            } else {
+                rows(0, 0);
+                rows(0, 1);
+                if (p.subs == 2) rows(1, 0), rows(1, 1);
+            }
+        };
+        int early = 0;   // stages whose B was requested before the wait
+        if (p.b_ready) {
+            early = first < n_tiles ? min(p.stages, k_end - k_begin) : 0;
+            int m0, n0;
+            tile_at(first, m0, n0);
+            if (elect_one())
+                for (int j = 0; j < early; ++j) load_b(j, k_begin + j, n0);
+            __syncwarp();
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            asm volatile("griddepcontrol.launch_dependents;");
+        }
         for (int t = first; t < n_tiles && ok; t += step) {
             int m0, n0;
             tile_at(t, m0, n0);
@@ -193,36 +250,9 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
             for (int kb = k_begin; kb < k_end; ++kb) {
                 ok = mbar_wait(&bar->empty[s], phase ^ 1);
                 if (!ok) break;
-                const int seg = kb >= p.kblocks, k0 = (kb - seg * p.kblocks) * BK;
-                uint8_t *sa = smem + s * p.stage_bytes, *sb = sa + GT_A;
                 if (elect_one()) {
-                    if (rank == 0) mbar_expect_tx(&bar->full[s], CG * p.stage_bytes);
-                    const uint32_t fb = CG == 2 ? map_rank(&bar->full[s], even) : su32(&bar->full[s]);
-                    const CUtensorMap *ma = &maps.a[seg];
-                    if constexpr (A_MN) {
-                        tma_load<CG>(sa, ma, m0, k0, fb);
-                        tma_load<CG>(sa + GT_A / 2, ma, m0 + 64, k0, fb);
-                    } else {
-                        tma_load<CG>(sa, ma, k0, m0, fb);
-                    }
-                    auto load_b = [&](int sub, int h) {   // half h of a sub-tile's rows
-                        const CUtensorMap *mb = EPI == EPI_GATE ? &maps.b[h] : &maps.b[seg];
-                        const int nb = EPI == EPI_GATE ? n0 + sub * half : n0 + sub * W + h * half;
-                        if constexpr (B_MN) {
-                            for (int c = 0; c < half; c += 64, sb += 64 * 128) tma_load<CG>(sb, mb, nb + c, k0, fb);
-                        } else {
-                            tma_load<CG>(sb, mb, k0, nb, fb);
-                            sb += half * 128;
-                        }
-                    };
-                    if constexpr (CG == 2) {
-                        load_b(0, rank);
-                        if (p.subs == 2) load_b(1, rank);
-                    } else {
-                        load_b(0, 0);
-                        load_b(0, 1);
-                        if (p.subs == 2) load_b(1, 0), load_b(1, 1);
-                    }
+                    if (filled >= early) load_b(s, kb, n0);
+                    load_a(s, kb, m0);
                 }
                 __syncwarp();
                 ++filled;
@@ -504,15 +534,17 @@ int launch_tc(const Maps &maps, const TileArgs &p, int clusters, cudaStream_t st
         __atomic_store_n(&ready[dev], 1, __ATOMIC_RELAXED);
     }
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     cfg.gridDim = dim3(clusters * CG * p.splits);
     cfg.blockDim = dim3(GT_NT);
     cfg.dynamicSmemBytes = GT_SMEM;
     cfg.stream = st;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim = {(unsigned)(CG * p.splits), 1, 1};
+    cfg.numAttrs = 2;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     QE_CHECK(cudaLaunchKernelEx(&cfg, kern, maps, p));
     QE_CHECK_LAUNCH("k_gemm_tc");
     return MOE_OK;
@@ -556,7 +588,7 @@ struct Shape {
 int choose(const GemmArgs &g, int ksteps, Shape *best) {
     long long least = -1;
     for (int cg = g.M > 128 ? 2 : 1; cg >= 1; --cg) {
-        const int tiles_m = (g.M + 128 * cg - 1) / (128 * cg);
+        const int tiles_m = (g.M + 128 * cg - 1) / (128 * cg), a_rows = std::min(g.M, 128);
         for (int splits = 1; splits <= 8 / cg && splits <= ksteps / 4 + 1; splits = splits < 4 ? splits + 1 : 2 * splits) {
             if ((splits - 1) * ((ksteps + splits - 1) / splits) >= ksteps) continue;   // no split without a k step
             int room = 0;
@@ -569,7 +601,7 @@ int choose(const GemmArgs &g, int ksteps, Shape *best) {
                     const long long tiles = (long long)tiles_m * ((g.N + out - 1) / out);
                     const long long waves = (tiles + room - 1) / room;
                     if (subs == 2 && waves > 1) continue;
-                    const long long step = std::max(2 * C, (GT_A + C * 128 / cg) / 64);
+                    const long long step = std::max(2 * C, (a_rows * GT_KB + C * GT_KB / cg) / 64);
                     const long long main = (long long)((ksteps + splits - 1) / splits) * step, epi = 24 * C;
                     long long t = 6000;
                     if (splits > 1) t += waves * (main + 3000 + 12 * C + epi / splits);
@@ -606,7 +638,7 @@ int read_dense_error(int *code) {
     return MOE_OK;
 }
 
-static int launch_shape(const GemmArgs &g, const Shape &sh, cudaStream_t st) {
+static int launch_shape(const GemmArgs &g, const Shape &sh, bool b_ready, cudaStream_t st) {
     const int bk = g.type == DT_S8 ? 128 : 64;
     Maps m;
     TileArgs p = {};
@@ -620,6 +652,8 @@ static int launch_shape(const GemmArgs &g, const Shape &sh, cudaStream_t st) {
     p.kper = (p.kblocks * g.segs + sh.splits - 1) / sh.splits;
     p.stage_bytes = GT_A + sh.W * sh.subs / cg * 128;
     p.stages = std::min(GT_MAX_STAGES, GT_RING / p.stage_bytes);
+    p.a_rows = cg == 1 && p.tiles_m == 1 ? (g.M + 7) / 8 * 8 : 128;   // whole 8-row swizzle groups
+    p.b_ready = b_ready;
     p.act = g.act;
     p.fp16 = g.type == MOE_FP16;
     p.out_dtype = g.out_dtype;
@@ -630,7 +664,7 @@ static int launch_shape(const GemmArgs &g, const Shape &sh, cudaStream_t st) {
     const int na = g.segs, nb = g.epi == EPI_GATE ? 2 : g.segs;
     for (int s = 0; s < na; ++s) {
         if (g.a_mn) QE_TRY(encode(&m.a[s], g.type, g.a[s], g.M, g.K, g.lda, 64, bk));
-        else QE_TRY(encode(&m.a[s], g.type, g.a[s], g.K, g.M, g.lda, bk, 128));
+        else QE_TRY(encode(&m.a[s], g.type, g.a[s], g.K, g.M, g.lda, bk, p.a_rows));
     }
     for (int s = 0; s < nb; ++s) {
         if (g.b_mn) QE_TRY(encode(&m.b[s], g.type, g.b[s], g.N, g.K, g.ldb, 64, bk));
@@ -653,7 +687,7 @@ int launch_gemm(const GemmArgs &g, Link link, cudaStream_t st) {
     const int bk = g.type == DT_S8 ? 128 : 64;
     Shape sh = {};
     QE_TRY(choose(g, (g.K + bk - 1) / bk * g.segs, &sh));
-    return launch_shape(g, sh, st);
+    return launch_shape(g, sh, link.b_ready, st);
 }
 
 }  // namespace qeffn
