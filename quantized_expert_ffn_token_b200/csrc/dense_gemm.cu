@@ -51,7 +51,7 @@ struct TileArgs {
     int tiles_m, tiles_n;
     int W, subs;                // sub-tile width, sub-tiles per tile
     int splits, kper;           // reduction splits (CTAs or pairs of a cluster), k steps each
-    int stages, stage_bytes;
+    int stages, stage_bytes, b_bytes;   // b_bytes: a sub-tile's B in one CTA
     int a_rows;                 // rows of an A box: fewer than 128 where all rows fit in one
     int b_ready;                // B does not depend on kernels of the same call: it may be loaded before the wait
     int act;
@@ -216,8 +216,8 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
             auto rows = [&](int sub, int h) {   // half h of a sub-tile's rows
                 const CUtensorMap *mb = EPI == EPI_GATE ? &maps.b[h] : &maps.b[seg];
                 const int nb = EPI == EPI_GATE ? n0 + sub * half : n0 + sub * W + h * half;
-                if constexpr (B_MN) {
-                    for (int c = 0; c < half; c += 64, sb += 64 * 128) tma_load<CG>(sb, mb, nb + c, k0, fb);
+                if constexpr (B_MN) {   // chunks of 64 rows; the pair's last chunk may be half used
+                    for (int c = 0; c < (CG == 2 ? half : W); c += 64, sb += 64 * 128) tma_load<CG>(sb, mb, nb + c, k0, fb);
                 } else {
                     tma_load<CG>(sb, mb, k0, nb, fb);
                     sb += half * 128;
@@ -226,6 +226,9 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
             if constexpr (CG == 2) {
                 rows(0, rank);
                 if (p.subs == 2) rows(1, rank);
+            } else if constexpr (B_MN) {
+                rows(0, 0);
+                if (p.subs == 2) rows(1, 0);
             } else {
                 rows(0, 0);
                 rows(0, 1);
@@ -292,7 +295,7 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
                     for (int j = 0; j < 4; ++j)
                         umma<S8, CG>(acc, ad + (A_MN ? 128 : 2) * j, bd + (B_MN ? 128 : 2) * j, idesc, kb > k_begin || j > 0);
                     if (p.subs == 2) {
-                        const uint64_t b1 = bd + ((uint32_t)(W / CG) * 128 >> 4);
+                        const uint64_t b1 = bd + (p.b_bytes >> 4);
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
                             umma<S8, CG>(acc + GT_W, ad + (A_MN ? 128 : 2) * j, b1 + (B_MN ? 128 : 2) * j, idesc, kb > k_begin || j > 0);
@@ -312,6 +315,8 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
 
     const int q = warp & 3, team = (warp - GT_EPI_W0) >> 2;   // epilogue: lane quarter, which of its two warps
     uint8_t *slot_buf = slots + (warp - GT_EPI_W0) * GT_SLOT;
+    // Splits: column of a partial tile in shared memory, the sub-tiles' columns following each other.
+    auto part_col = [&](int col) { return col < GT_W ? col : col - GT_W + W; };
     // Columns [col, col + 32) of this lane's accumulator row: from TMEM, or summed over the splits of the cluster.
     auto get = [&](uint32_t acc, int col, float (&v)[32]) {
         uint32_t r[32];
@@ -325,13 +330,18 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = 0.f;
             for (int j = 0; j < p.splits; ++j) {
-                const uint32_t src = map_rank(smem + (col * 128 + 32 * q + lane) * 4, j * CG + rank);
+                const uint32_t src = map_rank(smem + ((part_col(col) / 4) * 128 + 32 * q + lane) * 16, j * CG + rank);
+                uint4 w[8];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) r[i] = ld_cluster(src + i * 512);
+                for (int i = 0; i < 8; ++i) w[i] = ld_cluster(src + i * 2048);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    if constexpr (S8) sum[i] += (int)r[i];
-                    else v[i] += __uint_as_float(r[i]);
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t e[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if constexpr (S8) sum[4 * i + k] += (int)e[k];
+                        else v[4 * i + k] += __uint_as_float(e[k]);
+                    }
                 }
             }
             if constexpr (S8)
@@ -449,20 +459,20 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
             }
         }
     } else {
-        // one tile per cluster: every split leaves its accumulators in shared memory ([column][row], the ring is free
-        // once the last MMA has completed), and the splits share out the units
+        // one tile per cluster: every split leaves its accumulators in shared memory (16 bytes, four columns, a row; the
+        // ring is free once the last MMA has completed), and the splits share out the units
         int m0, n0;
         tile_at(first, m0, n0);
         m0 += rank * 128 + 32 * q;
         if (warp >= GT_EPI_W0 && mbar_wait(&bar->acc_full[0], 0)) {
             tc_fence_after();
-            for (int c = 32 * team; c < W; c += 64) {
+            for (int c = 32 * team; c < W * p.subs; c += 64) {
                 uint32_t r[32];
-                tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + c, r);
+                tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + (c < W ? c : c - W + GT_W), r);
                 tmem_wait();
-                uint32_t *dst = reinterpret_cast<uint32_t *>(smem) + c * 128 + 32 * q + lane;
+                uint4 *dst = reinterpret_cast<uint4 *>(smem) + (c / 4) * 128 + 32 * q + lane;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) dst[i * 128] = r[i];
+                for (int i = 0; i < 8; ++i) dst[i * 128] = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
             }
             tc_fence_before();
         }
@@ -470,7 +480,8 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
         if (warp >= GT_EPI_W0) {
             float rs = 1.f;
             if constexpr (S8) rs = m0 + lane < p.M ? p.row_scale[m0 + lane] : 0.f;
-            for (int u = split + p.splits * team; u < sub_units; u += 2 * p.splits) unit(0, 0, GT_UNIT * u, m0, n0, rs);
+            for (int u = split + p.splits * team; u < sub_units * p.subs; u += 2 * p.splits)
+                unit(0, u / sub_units, GT_UNIT * (u % sub_units), m0, n0, rs);
         }
     }
     if (warp >= GT_EPI_W0 && lane == 0) tma_wait_all();
@@ -581,35 +592,42 @@ struct Shape {
     int cg, W, subs, splits;
 };
 
+// Rows of B that a CTA loads for a sub-tile: whole chunks of 64 where the row index is contiguous.
+int b_rows(bool b_mn, int W, int cg) { return b_mn ? (W / cg + 63) / 64 * 64 : W / cg; }
+
 // The tile shape with the least modelled time, in SM cycles.  A k step takes the longer of its MMAs (2 cycles a column:
-// 128 rows x 64 values x 1 column at 4096 multiply-adds a cycle) and its loads (64 bytes a cycle from L2 to an SM); a
-// tile's epilogue about 24 cycles a column (measured between 15 for plain stores and 40 for the gate's gradient); a
-// launch about 6000 cycles of start and end.
+// 128 rows x 64 values x 1 column at 4096 multiply-adds a cycle) and its loads (72 bytes a cycle from L2 to an SM); a
+// tile's epilogue 2700 cycles and 14.5 a column (the gate's gradient, with its loads, 3.7 times that), hidden behind the
+// next tile where there is one; a split adds the exchange, 2000 cycles, 24.5 a column and 356 a CTA of the cluster; a
+// pair 1250 to start.  Fitted to 2,700 timings of 85 products (40 to 2,200 rows) on B200: the chosen shape is on average
+// 1.5 % and at most 17 % slower than the fastest one.
 int choose(const GemmArgs &g, int ksteps, Shape *best) {
     long long least = -1;
     for (int cg = g.M > 128 ? 2 : 1; cg >= 1; --cg) {
-        const int tiles_m = (g.M + 128 * cg - 1) / (128 * cg), a_rows = std::min(g.M, 128);
-        for (int splits = 1; splits <= 8 / cg && splits <= ksteps / 4 + 1; splits = splits < 4 ? splits + 1 : 2 * splits) {
-            if ((splits - 1) * ((ksteps + splits - 1) / splits) >= ksteps) continue;   // no split without a k step
+        const int tiles_m = (g.M + 128 * cg - 1) / (128 * cg), a_rows = g.a_mn ? 128 : std::min(g.M, 128);
+        for (int splits = 1; splits <= 8 / cg && splits <= ksteps; splits = splits < 4 ? splits + 1 : 2 * splits) {
+            const int kper = (ksteps + splits - 1) / splits;
+            if ((splits - 1) * kper >= ksteps) continue;   // no split without a k step
             int room = 0;
             QE_TRY(active_clusters(cg * splits, &room));
-            for (int subs = 1; subs <= (splits == 1 ? 2 : 1); ++subs) {
-                // sub-tile widths: halves of whole 32-column units (gate), of 64 rows where B has its row index contiguous
-                const int unit = g.b_mn ? 128 : g.epi == EPI_GATE ? 64 : 32;
-                for (int W = subs == 2 ? 128 + unit : unit; W <= GT_W; W += unit) {
+            for (int subs = 1; subs <= 2; ++subs) {
+                // sub-tile widths: whole 32-column units of both halves (gate), 64 rows where B's row index is contiguous
+                const int unit = g.b_mn || g.epi == EPI_GATE ? 64 : 32;
+                for (int W = unit; W <= GT_W; W += unit) {
                     const int C = W * subs, out = g.epi == EPI_GATE ? C / 2 : C;
-                    const long long tiles = (long long)tiles_m * ((g.N + out - 1) / out);
-                    const long long waves = (tiles + room - 1) / room;
-                    if (subs == 2 && waves > 1) continue;
-                    const long long step = std::max(2 * C, (a_rows * GT_KB + C * GT_KB / cg) / 64);
-                    const long long main = (long long)((ksteps + splits - 1) / splits) * step, epi = 24 * C;
-                    long long t = 6000;
-                    if (splits > 1) t += waves * (main + 3000 + 12 * C + epi / splits);
+                    const int tiles_n = (g.N + out - 1) / out, waves = (int)(((long long)tiles_m * tiles_n + room - 1) / room);
+                    if (splits > 1 && C * 512 > GT_RING) break;    // the partial tile has to fit
+                    const int step = std::max(2 * C, (a_rows + subs * b_rows(g.b_mn, W, cg)) * GT_KB / 72);
+                    const long long main = (long long)kper * step, epi = 2700 + C * (g.epi == EPI_GATE_BWD ? 54 : 29 / 2);
+                    long long t = cg == 2 ? 1250 : 0;
+                    if (splits > 1) t += waves * (main + 2000 + 49 * C / 2 + 356 * cg * splits + epi / splits);
+                    else if (subs == 2) t += waves * (main + epi);
                     else t += (waves - 1) * std::max(main, epi) + main + epi;
                     if (least < 0 || t < least) {
                         least = t;
                         *best = {cg, W, subs, splits};
                     }
+                    if (tiles_n == 1) break;   // wider tiles only waste columns
                 }
             }
         }
@@ -650,7 +668,8 @@ static int launch_shape(const GemmArgs &g, const Shape &sh, bool b_ready, cudaSt
     p.tiles_n = (g.N + tn - 1) / tn;
     p.W = sh.W, p.subs = sh.subs, p.splits = sh.splits;
     p.kper = (p.kblocks * g.segs + sh.splits - 1) / sh.splits;
-    p.stage_bytes = GT_A + sh.W * sh.subs / cg * 128;
+    p.b_bytes = b_rows(g.b_mn, sh.W, cg) * GT_KB;
+    p.stage_bytes = GT_A + sh.subs * p.b_bytes;
     p.stages = std::min(GT_MAX_STAGES, GT_RING / p.stage_bytes);
     p.a_rows = cg == 1 && p.tiles_m == 1 ? (g.M + 7) / 8 * 8 : 128;   // whole 8-row swizzle groups
     p.b_ready = b_ready;
