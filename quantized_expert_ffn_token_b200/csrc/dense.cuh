@@ -52,8 +52,8 @@ struct GemmArgs {
 struct Link {
     bool b_ready = false;   // a later kernel of the call, and B is an input of the call
 };
-constexpr int kFewRows = 32;   // products of at most this many rows stream the weights (dense_rows.cu)
 int launch_gemm(const GemmArgs &g, Link link, cudaStream_t st);
+bool rows_fit(const GemmArgs &g);   // the product streams its weights (dense_rows.cu) rather than tiling them
 int launch_rows(const GemmArgs &g, Link link, cudaStream_t st);
 int read_dense_error(int *code);   // reads and clears the error word of the current device
 int launch_quantize_s8(const void *x, int dtype, long long ld, int rows, int cols, int8_t *q, float *scale,

@@ -702,7 +702,7 @@ static int launch_shape(const GemmArgs &g, const Shape &sh, bool b_ready, cudaSt
 }
 
 int launch_gemm(const GemmArgs &g, Link link, cudaStream_t st) {
-    if (g.M <= kFewRows && !g.a_mn && !g.b_mn && g.segs == 1) return launch_rows(g, link, st);
+    if (rows_fit(g)) return launch_rows(g, link, st);
     const int bk = g.type == DT_S8 ? 128 : 64;
     Shape sh = {};
     QE_TRY(choose(g, (g.K + bk - 1) / bk * g.segs, &sh));

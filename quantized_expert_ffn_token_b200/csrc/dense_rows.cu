@@ -180,26 +180,23 @@ int launch_rows_as(const RowsArgs &p, cudaStream_t st) {
     return MOE_OK;
 }
 
-// Shapes, measured on B200 (bf16 unless said; GB/s of weights, launches back to back, each waiting for the last):
-//   one token, gate and up 2 x 10240 x 2560: 8 warps, 2 CTAs per SM 6000 (3: 5620, 4 warps x 6: 5270, 16 x 2: 5130)
-//   one token, 2560 x 10240: 8 warps with 4 blocks in flight 4410 (2 blocks: 4000, 4 warps: 3180, 16 warps: 3840)
-//   a grid below the SM count (2 x 512 x 2560): 16 warps 1600, 8 warps 1410
-//   16 tokens: two row groups a CTA, because the token operand costs as much as the weights: 10240 x 2560 8-bit 4 warps
-//   x 6 CTAs 3280 (one group: 2750); rows of 64 blocks and more want 16 warps (2560 x 10240: 3100, 8 warps 2510)
+// Shapes, measured on B200 (launches back to back, each waiting for the last; bf16 unless said):
+//   one token, gate and up 2 x 10240 x 2560: 8 warps, 2 CTAs per SM 6000 GB/s (3: 5620, 4 warps x 6: 5270, 16 x 2: 5130)
+//   one token, 2560 x 10240: 8 warps with 4 blocks in flight 4410 GB/s (2 blocks: 4000, 4 warps: 3180, 16 warps: 3840)
+//   a grid below the SM count: 16 warps (2 x 512 x 2560, one token: 1600 GB/s, 8 warps 1410; 1024 x 6000, 12 tokens: 6.2
+//   us, 8 warps 7.7; two row groups a CTA 7.6)
+//   several tokens, more rows than that: two row groups a CTA, because the token operand costs as much as the weights;
+//   16 warps for up to 4096 rows or rows of 64 blocks (2048 x 1024, 32 tokens: 2.9 us, one group 3.8; 2560 x 10240, 16
+//   tokens: 16.9, 8 warps 20.9), else 4 warps (10240 x 2560 8-bit, 16 tokens: 8.0, one group 9.5, 16 warps 10.8)
 template <int TYPE, int TT>
 int launch_rows_t(const RowsArgs &p, bool gate, cudaStream_t st) {
-    const bool few = p.N <= 8 * 148, longrow = p.Kb >= 64 * 128;
-    if (gate) {
-        if (few) return launch_rows_as<TYPE, TT, true, 1, 16, 1, 1>(p, st);
-        return launch_rows_as<TYPE, TT, true, 1, 8, 1, TT == 1 ? 2 : 3>(p, st);
-    }
-    if constexpr (TT == 1) {
-        if (few) return launch_rows_as<TYPE, TT, false, 1, 16, 2, 1>(p, st);
-        return launch_rows_as<TYPE, TT, false, 1, 8, 4, 3>(p, st);
-    } else {
-        if (few || longrow) return launch_rows_as<TYPE, TT, false, 2, 16, 1, 2>(p, st);
-        return launch_rows_as<TYPE, TT, false, 2, 4, 1, 6>(p, st);
-    }
+    const bool few = p.N <= 8 * 148;
+    if (gate)
+        return few ? launch_rows_as<TYPE, TT, true, 1, 16, 1, 1>(p, st) : launch_rows_as<TYPE, TT, true, 1, 8, 1, 2>(p, st);
+    if (few) return launch_rows_as<TYPE, TT, false, 1, 16, 2, 1>(p, st);
+    if constexpr (TT == 1) return launch_rows_as<TYPE, TT, false, 1, 8, 4, 3>(p, st);
+    if (p.N <= 4096 || p.Kb >= 64 * 128) return launch_rows_as<TYPE, TT, false, 2, 16, 1, 2>(p, st);
+    return launch_rows_as<TYPE, TT, false, 2, 4, 1, 6>(p, st);
 }
 
 template <int TYPE>
@@ -209,6 +206,14 @@ int launch_rows_type(const RowsArgs &p, bool gate, cudaStream_t st) {
 }
 
 }  // namespace
+
+// Which products these are.  Up to 16 rows always; up to 32 while the weights are few, where the launch counts: a 512 x
+// 512 block at 32 rows took 4.4 us (tensor-core tiles 8.5), 1024 x 2048 9.9 (12.9), 2560 x 10240 51 (38).
+bool rows_fit(const GemmArgs &g) {
+    if (g.a_mn || g.b_mn || g.segs != 1) return false;
+    const long long bytes = (long long)g.N * g.K * (g.type == DT_S8 ? 1 : 2) * (g.epi == EPI_GATE ? 2 : 1);
+    return g.M <= 16 || (g.M <= 32 && bytes <= 24LL << 20);
+}
 
 int launch_rows(const GemmArgs &g, Link link, cudaStream_t st) {
     const int size = g.type == DT_S8 ? 1 : 2;
