@@ -168,6 +168,12 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 2) tmem_alloc<CG>(&bar->tmem, 2 * GT_W);
+    if (warp == 3 && lane < 7) {   // the copies' descriptors
+        const CUtensorMap *m = lane < 2 ? &maps.a[lane] : lane < 4 ? &maps.b[lane - 2] : &maps.out[lane - 4];
+        const bool used = lane == 0 || lane == 2 || (lane == 1 && p.segs == 2) || (lane == 3 && (p.segs == 2 || EPI == EPI_GATE)) ||
+                          lane == 4 || (p.extra && EPI == EPI_GATE) || (EPI == EPI_GATE_BWD && (lane == 5 || p.extra));
+        if (used) prefetch_map(m);
+    }
     tc_fence_before();
     __syncthreads();
     if (CG * p.splits > 1) cluster_sync();
@@ -484,7 +490,7 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
                 unit(0, u / sub_units, GT_UNIT * (u % sub_units), m0, n0, rs);
         }
     }
-    if (warp >= GT_EPI_W0 && lane == 0) tma_wait_all();
+    if (warp >= GT_EPI_W0 && lane == 0) tma_wait_read<0>();   // the stores have read shared memory; the grid's end completes them
     __syncwarp();
     tc_fence_before();
     __syncthreads();
