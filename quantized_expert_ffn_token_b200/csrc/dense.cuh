@@ -42,19 +42,20 @@ struct GemmArgs {
     const float *col_scale[2] = {nullptr, nullptr};      // [N], EPI_GATE: of gate and up
     const float *bias = nullptr;                         // [N] or NULL
     bool add = false;             // EPI_STORE with fp32 out: out += C
+    bool b_ready = false;         // a later kernel of its call, and B is an input of the call
 };
 
-// Position of a product in its call.  Every kernel here is launched programmatically: it starts while the kernel before
-// it drains, waits for that one's results before it touches them, and only then lets the next kernel start; so when a
-// later kernel of a call runs, everything before the call is complete.  A call's first kernel reads nothing before its
-// wait, because the kernel before it may be the one that writes its inputs; a later one may load operands that are
-// inputs of the call.
-struct Link {
-    bool b_ready = false;   // a later kernel of the call, and B is an input of the call
-};
-int launch_gemm(const GemmArgs &g, Link link, cudaStream_t st);
+// Kernels of one call and of calls after each other overlap.  Every kernel here is launched programmatically: it starts
+// while the kernel before it drains, waits for that one's results before it touches them, and only then lets the next
+// kernel start; so when a later kernel of a call runs, everything before the call is complete.  A call's first kernel
+// reads nothing before its wait, because the kernel before it may be the one that writes its inputs; a later one may load
+// operands that are inputs of the call (GemmArgs::b_ready).
+int launch_gemm(const GemmArgs &g, cudaStream_t st);
+int launch_rows(const GemmArgs &g, cudaStream_t st);
+constexpr int kGroup = 4;
+// The gradients' products (dx may be NULL, n_dw at most 3), in one launch or two.
+int launch_gradients(const GemmArgs *dx, const GemmArgs *dw, int n_dw, cudaStream_t st);
 bool rows_fit(const GemmArgs &g);   // the product streams its weights (dense_rows.cu) rather than tiling them
-int launch_rows(const GemmArgs &g, Link link, cudaStream_t st);
 int read_dense_error(int *code);   // reads and clears the error word of the current device
 int launch_quantize_s8(const void *x, int dtype, long long ld, int rows, int cols, int8_t *q, float *scale,
                        cudaStream_t st);

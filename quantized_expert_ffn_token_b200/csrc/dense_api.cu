@@ -159,7 +159,7 @@ int moe_ffn_forward(const moe_ffn *f, const void *x, long long ld_x, int T, void
     g.b[0] = f->w_gate, g.b[1] = f->w_up, g.ldb = d;
     g.epi = EPI_GATE, g.act = f->act;
     g.out = w.h, g.out_dtype = f->dtype, g.ldo = I, g.out1 = gate, g.out2 = up;
-    QE_TRY(launch_gemm(g, {}, st));
+    QE_TRY(launch_gemm(g, st));
 
     GemmArgs y2;
     y2.type = f->dtype;
@@ -167,7 +167,8 @@ int moe_ffn_forward(const moe_ffn *f, const void *x, long long ld_x, int T, void
     y2.a[0] = w.h, y2.lda = I;
     y2.b[0] = f->w_down, y2.ldb = I;
     y2.out = y, y2.out_dtype = f->dtype, y2.ldo = ly;
-    return launch_gemm(y2, {true}, st);
+    y2.b_ready = true;
+    return launch_gemm(y2, st);
 }
 
 int moe_ffn_backward(const moe_ffn *f, const void *x, long long ld_x, const void *gate, const void *up, const void *dy,
@@ -211,35 +212,33 @@ int moe_ffn_backward(const moe_ffn *f, const void *x, long long ld_x, const void
     g.epi = EPI_GATE_BWD, g.act = f->act;
     g.in1 = gate, g.in2 = up;
     g.out = w.dg, g.out_dtype = f->dtype, g.ldo = I, g.out1 = w.du, g.out2 = dw ? w.h : nullptr;
-    QE_TRY(launch_gemm(g, {}, st));
+    QE_TRY(launch_gemm(g, st));
 
-    if (dx) {
-        GemmArgs p;
-        p.type = f->dtype;
-        p.M = T, p.N = d, p.K = I, p.segs = 2;
-        p.a[0] = w.dg, p.a[1] = w.du, p.lda = I;
-        p.b[0] = f->w_gate, p.b[1] = f->w_up, p.ldb = d, p.b_mn = true;
-        p.out = dx, p.out_dtype = f->dtype, p.ldo = ldx;
-        QE_TRY(launch_gemm(p, {true}, st));
-    }
-    if (dw) {
-        GemmArgs p;
+    GemmArgs px;
+    px.type = f->dtype;
+    px.M = T, px.N = d, px.K = I, px.segs = 2;
+    px.a[0] = w.dg, px.a[1] = w.du, px.lda = I;
+    px.b[0] = f->w_gate, px.b[1] = f->w_up, px.ldb = d, px.b_mn = true, px.b_ready = true;
+    px.out = dx, px.out_dtype = f->dtype, px.ldo = ldx;
+    GemmArgs pw[3];   // gate, up, down
+    for (int i = 0; i < 3; ++i) {
+        GemmArgs &p = pw[i];
         p.type = f->dtype;
         p.K = T;
         p.a_mn = p.b_mn = true;
         p.out_dtype = f32 ? (int)MOE_FP32 : f->dtype;
         p.add = add;
-        p.M = I, p.N = d, p.lda = I, p.ldb = lx, p.ldo = d;
-        p.b[0] = x;
-        p.a[0] = w.dg, p.out = dw_gate;
-        QE_TRY(launch_gemm(p, {true}, st));
-        p.a[0] = w.du, p.out = dw_up;
-        QE_TRY(launch_gemm(p, {true}, st));
-        p.M = d, p.N = I, p.lda = ldy, p.ldb = I, p.ldo = I;
-        p.a[0] = dy, p.b[0] = w.h, p.out = dw_down;
-        QE_TRY(launch_gemm(p, {}, st));
+        if (i < 2) {
+            p.M = I, p.N = d, p.lda = I, p.ldb = lx, p.ldo = d;
+            p.a[0] = i == 0 ? w.dg : w.du, p.b[0] = x, p.b_ready = true;
+            p.out = i == 0 ? dw_gate : dw_up;
+        } else {
+            p.M = d, p.N = I, p.lda = ldy, p.ldb = I, p.ldo = I;
+            p.a[0] = dy, p.b[0] = w.h;
+            p.out = dw_down;
+        }
     }
-    return MOE_OK;
+    return launch_gradients(dx ? &px : nullptr, pw, dw ? 3 : 0, st);
 }
 
 int moe_quantize_s8(const void *x, int dtype, long long ld_x, int rows, int cols, int8_t *q, float *scale,
@@ -286,7 +285,7 @@ int moe_matmul_s8(const int8_t *a, const float *a_scale, int T, const int8_t *w,
     g.a[0] = a, g.lda = K, g.b[0] = w, g.ldb = K;
     g.row_scale = a_scale, g.col_scale[0] = w_scale, g.bias = bias;
     g.out = y, g.out_dtype = y_dtype, g.ldo = ly;
-    return launch_gemm(g, {}, (cudaStream_t)stream);
+    return launch_gemm(g, (cudaStream_t)stream);
 }
 
 int moe_ffn_s8_workspace(const moe_ffn_s8 *f, int T, long long *bytes) {
@@ -323,7 +322,8 @@ int moe_ffn_s8_forward(const moe_ffn_s8 *f, const void *x, long long ld_x, int T
     g.row_scale = w.xs, g.col_scale[0] = f->s_gate, g.col_scale[1] = f->s_up;
     g.epi = EPI_GATE, g.act = f->act;
     g.out = w.h, g.out_dtype = MOE_FP32, g.ldo = I;
-    QE_TRY(launch_gemm(g, {true}, st));
+    g.b_ready = true;
+    QE_TRY(launch_gemm(g, st));
     QE_TRY(launch_quantize_s8(w.h, MOE_FP32, I, T, I, w.hq, w.hs, st));
     GemmArgs p;
     p.type = DT_S8;
@@ -331,7 +331,8 @@ int moe_ffn_s8_forward(const moe_ffn_s8 *f, const void *x, long long ld_x, int T
     p.a[0] = w.hq, p.lda = I, p.b[0] = f->w_down, p.ldb = I;
     p.row_scale = w.hs, p.col_scale[0] = f->s_down;
     p.out = y, p.out_dtype = f->dtype, p.ldo = ly;
-    return launch_gemm(p, {true}, st);
+    p.b_ready = true;
+    return launch_gemm(p, st);
 }
 
 int moe_ffn_get_device_error(int *code) {

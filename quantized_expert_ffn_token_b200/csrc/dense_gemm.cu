@@ -42,25 +42,64 @@ constexpr int GT_UNIT = 32;                 // columns an epilogue warp handles 
 constexpr int GT_SLOT = 6144;               // an epilogue warp's store tiles: three of 32 rows x 64 bytes (one of fp32)
 constexpr int GT_SMEM = 1024 + GT_RING + GT_EPI_NW * GT_SLOT + 256;
 
+// A launch is one product, or a group of up to four that share the tile shape (the gradients).
+template <int NG>
 struct Maps {
-    CUtensorMap a[2], b[2], out[3];
+    CUtensorMap a[NG][2], b[NG][2], out[NG > 3 ? NG : 3];   // out: of one product's up to three outputs, or of each product
 };
 
-struct TileArgs {
+struct Product {
     int M, N, kblocks, segs;    // kblocks: k steps of one segment
-    int tiles_m, tiles_n;
+    int tiles_m, tiles_n, start;   // start: index of its first tile
+    int a_mn;
+    int a_rows;                 // rows of an A box: fewer than 128 where all rows fit in one
+    int b_ready;                // B does not depend on kernels of the same call: it may be loaded before the wait
+    int out_dtype, add;
+};
+
+template <int NG>
+struct TileArgs {
+    Product prod[NG];
+    int products, tiles;        // tiles of all products
+    int big, rounds;            // order of the tiles, see Order
     int W, subs;                // sub-tile width, sub-tiles per tile
     int splits, kper;           // reduction splits (CTAs or pairs of a cluster), k steps each
     int stages, stage_bytes, b_bytes;   // b_bytes: a sub-tile's B in one CTA
-    int a_rows;                 // rows of an A box: fewer than 128 where all rows fit in one
-    int b_ready;                // B does not depend on kernels of the same call: it may be loaded before the wait
     int act;
     int fp16;                   // 16-bit operands (and out1, out2): fp16 rather than bf16
-    int out_dtype;
-    int add;
+    int rotate;                 // 16-bit outputs throughout, one a tile: the store tiles take turns
     int extra;                  // out1 and out2 wanted (EPI_GATE: both, EPI_GATE_BWD: out2)
     const void *in1, *in2;
     const float *row_scale, *col_scale0, *col_scale1, *bias;
+};
+
+// The tiles of cluster c of P, in order.  The first `big` tiles (a product with a long reduction) are dealt round robin;
+// so the first big % P clusters hold one more of them, and the others take `rounds` more of the remaining tiles, which
+// are dealt round robin among those that have time.
+template <int NG>
+struct Order {
+    int c, P, n, mine, rest, rounds;
+    bool more;
+    __device__ Order(const TileArgs<NG> &p, int cluster, int clusters) : c(cluster), P(clusters), n(p.tiles) {
+        if constexpr (NG > 1) {
+            mine = c < p.big ? (p.big - c + P - 1) / P : 0;
+            const int r = p.big % P;
+            rest = P - r;
+            more = c >= r;
+            rounds = p.rounds;
+            big = p.big;
+        }
+    }
+    int big = 0;
+    __device__ int at(int k) const {   // -1: no more
+        int t = c + k * P;
+        if constexpr (NG > 1)
+            if (k >= mine) {
+                const int j = k - mine;
+                t = big + (more && j < rounds ? j * rest + c - (P - rest) : rounds * rest + (j - (more ? rounds : 0)) * P + c);
+            }
+        return t < n ? t : -1;
+    }
 };
 
 struct GtBars {
@@ -139,8 +178,9 @@ __device__ __forceinline__ void gate_bwd_all(int act, float (&v)[32], float (&u)
     else gate_bwd_as<MOE_ACT_GELU>(v, u, g);
 }
 
-template <bool S8, bool A_MN, bool B_MN, int EPI, int CG>
-__global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Maps maps, const __grid_constant__ TileArgs p) {
+// A_MN: A's row index is contiguous (0, 1; 2: as each product of the group says).
+template <bool S8, int A_MN, bool B_MN, int EPI, int CG, int NG>
+__global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Maps<NG> maps, const __grid_constant__ TileArgs<NG> p) {
     constexpr int BK = S8 ? 128 : 64;             // reduction values per stage
     constexpr int TM = 128 * CG;                  // rows of a tile
     extern __shared__ uint8_t smem_raw[];
@@ -168,59 +208,76 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 2) tmem_alloc<CG>(&bar->tmem, 2 * GT_W);
-    if (warp == 3 && lane < 7) {   // the copies' descriptors
-        const CUtensorMap *m = lane < 2 ? &maps.a[lane] : lane < 4 ? &maps.b[lane - 2] : &maps.out[lane - 4];
-        const bool used = lane == 0 || lane == 2 || (lane == 1 && p.segs == 2) || (lane == 3 && (p.segs == 2 || EPI == EPI_GATE)) ||
-                          lane == 4 || (p.extra && EPI == EPI_GATE) || (EPI == EPI_GATE_BWD && (lane == 5 || p.extra));
-        if (used) prefetch_map(m);
+    if (warp == 3) {   // the copies' descriptors
+        if (lane < 2 * p.products && (lane % 2 == 0 || p.prod[lane / 2].segs == 2)) prefetch_map(&maps.a[lane / 2][lane % 2]);
+        if (lane < 2 * p.products && (lane % 2 == 0 || p.prod[lane / 2].segs == 2 || EPI == EPI_GATE))
+            prefetch_map(&maps.b[lane / 2][lane % 2]);
+        const int outs = EPI == EPI_STORE ? p.products : EPI == EPI_GATE ? (p.extra ? 3 : 1) : p.extra ? 3 : 2;
+        if (lane < outs) prefetch_map(&maps.out[lane]);
     }
     tc_fence_before();
     __syncthreads();
     if (CG * p.splits > 1) cluster_sync();
     tc_fence_after();
     const uint32_t tmem = bar->tmem;
+    const Order<NG> order(p, blockIdx.x / (CG * p.splits), gridDim.x / (CG * p.splits));
+    // tiles of a product in bands of 8 row blocks, so that the tiles in flight share rows of both operands in L2
+    auto tile_at = [&](int t, int &m0, int &n0) {
+        int g = 0;
+        if constexpr (NG > 1)
+            while (g + 1 < p.products && t >= p.prod[g + 1].start) ++g;
+        const Product &pr = p.prod[g];
+        t -= pr.start;
+        const int band = t / (8 * pr.tiles_n), in = t - band * 8 * pr.tiles_n;
+        const int rows = min(8, pr.tiles_m - 8 * band);
+        m0 = (8 * band + in % rows) * TM;
+        n0 = (in / rows) * tile_cols;
+        return g;
+    };
+    const int k_begin = split * p.kper;
+    auto k_end_of = [&](const Product &pr) { return min(pr.kblocks * pr.segs, k_begin + p.kper); };
+    auto a_mn = [&](const Product &pr) { return A_MN == 2 ? pr.a_mn != 0 : A_MN == 1; };
+
     // programmatic launch: all of the above overlapped the kernel before; its results are touched from here on (the
     // producer of a product whose B is an input of the call first fills the ring with B)
-    if (!(warp == 0 && p.b_ready)) {
+    bool b_early = false;
+    int t0 = 0;
+    if (warp == 0) {
+        t0 = order.at(0);
+        int m0, n0;
+        b_early = t0 >= 0 && p.prod[tile_at(t0, m0, n0)].b_ready;
+    }
+    if (!b_early) {
         asm volatile("griddepcontrol.wait;" ::: "memory");
         asm volatile("griddepcontrol.launch_dependents;");
     }
-
-    const int n_tiles = p.tiles_m * p.tiles_n;
-    const int first = blockIdx.x / (CG * p.splits), step = gridDim.x / (CG * p.splits);
-    const int k_begin = split * p.kper, k_end = min(p.kblocks * p.segs, k_begin + p.kper);
-    // tiles in bands of 8 row blocks, so that the tiles in flight share rows of both operands in L2
-    auto tile_at = [&](int t, int &m0, int &n0) {
-        const int band = t / (8 * p.tiles_n), in = t - band * 8 * p.tiles_n;
-        const int rows = min(8, p.tiles_m - 8 * band);
-        m0 = (8 * band + in % rows) * TM;
-        n0 = (in / rows) * tile_cols;
-    };
 
     if (warp == 0) {
         int s = 0, filled = 0;
         uint32_t phase = 0;
         bool ok = true;
-        const uint32_t a_bytes = A_MN ? GT_A : p.a_rows * GT_KB;
-        // copies of k step kb of tile (m0, n0) into stage s: A's and B's (by the elected lane)
-        auto load_a = [&](int st, int kb, int m0) {
-            const int seg = kb >= p.kblocks, k0 = (kb - seg * p.kblocks) * BK;
+        // copies of k step kb of tile (m0, n0) into stage st: A's and B's (by the elected lane)
+        auto load_a = [&](int st, int g, int kb, int m0) {
+            const Product &pr = p.prod[g];
+            const int seg = kb >= pr.kblocks, k0 = (kb - seg * pr.kblocks) * BK;
             uint8_t *sa = smem + st * p.stage_bytes;
             const uint32_t fb = CG == 2 ? map_rank(&bar->full[st], even) : su32(&bar->full[st]);
-            if constexpr (A_MN) {
-                tma_load<CG>(sa, &maps.a[seg], m0, k0, fb);
-                tma_load<CG>(sa + GT_A / 2, &maps.a[seg], m0 + 64, k0, fb);
+            if (a_mn(pr)) {
+                tma_load<CG>(sa, &maps.a[g][seg], m0, k0, fb);
+                tma_load<CG>(sa + GT_A / 2, &maps.a[g][seg], m0 + 64, k0, fb);
             } else {
-                tma_load<CG>(sa, &maps.a[seg], k0, m0, fb);
+                tma_load<CG>(sa, &maps.a[g][seg], k0, m0, fb);
             }
         };
-        auto load_b = [&](int st, int kb, int n0) {
-            const int seg = kb >= p.kblocks, k0 = (kb - seg * p.kblocks) * BK;
+        auto load_b = [&](int st, int g, int kb, int n0) {
+            const Product &pr = p.prod[g];
+            const int seg = kb >= pr.kblocks, k0 = (kb - seg * pr.kblocks) * BK;
             uint8_t *sb = smem + st * p.stage_bytes + GT_A;
             const uint32_t fb = CG == 2 ? map_rank(&bar->full[st], even) : su32(&bar->full[st]);
+            const int a_bytes = a_mn(pr) ? GT_A : pr.a_rows * GT_KB;
             if (rank == 0) mbar_expect_tx(&bar->full[st], CG * (p.stage_bytes - GT_A + a_bytes));
             auto rows = [&](int sub, int h) {   // half h of a sub-tile's rows
-                const CUtensorMap *mb = EPI == EPI_GATE ? &maps.b[h] : &maps.b[seg];
+                const CUtensorMap *mb = EPI == EPI_GATE ? &maps.b[g][h] : &maps.b[g][seg];
                 const int nb = EPI == EPI_GATE ? n0 + sub * half : n0 + sub * W + h * half;
                 if constexpr (B_MN) {   // chunks of 64 rows; the pair's last chunk may be half used
                     for (int c = 0; c < (CG == 2 ? half : W); c += 64, sb += 64 * 128) tma_load<CG>(sb, mb, nb + c, k0, fb);
@@ -242,26 +299,27 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
             }
         };
         int early = 0;   // stages whose B was requested before the wait
-        if (p.b_ready) {
-            early = first < n_tiles ? min(p.stages, k_end - k_begin) : 0;
+        if (b_early) {
             int m0, n0;
-            tile_at(first, m0, n0);
+            const int g = tile_at(t0, m0, n0);
+            early = min(p.stages, k_end_of(p.prod[g]) - k_begin);
             if (elect_one())
-                for (int j = 0; j < early; ++j) load_b(j, k_begin + j, n0);
+                for (int j = 0; j < early; ++j) load_b(j, g, k_begin + j, n0);
             __syncwarp();
             asm volatile("griddepcontrol.wait;" ::: "memory");
             asm volatile("griddepcontrol.launch_dependents;");
         }
-        for (int t = first; t < n_tiles && ok; t += step) {
+        for (int k = 0, t; ok && (t = order.at(k)) >= 0; ++k) {
             int m0, n0;
-            tile_at(t, m0, n0);
+            const int g = tile_at(t, m0, n0);
             m0 += rank * 128;
+            const int k_end = k_end_of(p.prod[g]);
             for (int kb = k_begin; kb < k_end; ++kb) {
                 ok = mbar_wait(&bar->empty[s], phase ^ 1);
                 if (!ok) break;
                 if (elect_one()) {
-                    if (filled >= early) load_b(s, kb, n0);
-                    load_a(s, kb, m0);
+                    if (filled >= early) load_b(s, g, kb, n0);
+                    load_a(s, g, kb, m0);
                 }
                 __syncwarp();
                 ++filled;
@@ -279,32 +337,37 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
     } else if (warp == 1 && rank == 0) {
         const uint32_t idesc = (S8 ? (2u << 4) | (1u << 7) | (1u << 10)
                                    : (1u << 4) | (p.fp16 ? 0u : (1u << 7) | (1u << 10))) |
-                               (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u) | ((uint32_t)(W >> 3) << 17) |
+                               (B_MN ? 1u << 16 : 0u) | ((uint32_t)(W >> 3) << 17) |
                                ((uint32_t)(TM >> 4) << 24);
         int s = 0, n = 0;
         uint32_t phase = 0;
         bool ok = true;
-        for (int t = first; t < n_tiles && ok; t += step, ++n) {
+        for (int t; ok && (t = order.at(n)) >= 0; ++n) {
             const int slot = two_acc ? n & 1 : 0, use = two_acc ? n >> 1 : n;
             ok = mbar_wait(&bar->acc_empty[slot], (use & 1) ^ 1);
             if (!ok) break;
             tc_fence_after();
+            int m0, n0;
+            const Product &pr = p.prod[tile_at(t, m0, n0)];
+            const int k_end = k_end_of(pr);
+            const bool amn = a_mn(pr);
+            const uint32_t id = idesc | (amn ? 1u << 15 : 0u), a_lead = amn ? 64 * 128 : 16, a_step = amn ? 128 : 2;
             for (int kb = k_begin; kb < k_end; ++kb) {
                 ok = mbar_wait(&bar->full[s], phase);
                 if (!ok) break;
                 tc_fence_after();
                 // 32 bytes of k at a time: within the 128-byte rows, or 16 of the 128-byte rows
                 const uint32_t a0 = su32(smem + s * p.stage_bytes), acc = tmem + GT_W * slot;
-                const uint64_t ad = smem_desc(a0, A_MN ? 64 * 128 : 16), bd = smem_desc(a0 + GT_A, B_MN ? 64 * 128 : 16);
+                const uint64_t ad = smem_desc(a0, a_lead), bd = smem_desc(a0 + GT_A, B_MN ? 64 * 128 : 16);
                 if (elect_one()) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        umma<S8, CG>(acc, ad + (A_MN ? 128 : 2) * j, bd + (B_MN ? 128 : 2) * j, idesc, kb > k_begin || j > 0);
+                        umma<S8, CG>(acc, ad + a_step * j, bd + (B_MN ? 128 : 2) * j, id, kb > k_begin || j > 0);
                     if (p.subs == 2) {
                         const uint64_t b1 = bd + (p.b_bytes >> 4);
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            umma<S8, CG>(acc + GT_W, ad + (A_MN ? 128 : 2) * j, b1 + (B_MN ? 128 : 2) * j, idesc, kb > k_begin || j > 0);
+                            umma<S8, CG>(acc + GT_W, ad + a_step * j, b1 + (B_MN ? 128 : 2) * j, id, kb > k_begin || j > 0);
                     }
                     umma_commit<CG>(&bar->empty[s], even);
                 }
@@ -356,42 +419,41 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
         }
     };
     // Store tiles: three 16-bit ones in turn where a unit has one output, else all at once.
-    const bool rotate = (EPI == EPI_STORE && p.out_dtype != MOE_FP32) || (EPI == EPI_GATE && !S8 && !p.extra);
     int turn = 0;
     auto acquire = [&]() {
         if (lane == 0) {
-            if (rotate) tma_wait_read<2>();
+            if (p.rotate) tma_wait_read<2>();
             else tma_wait_read<0>();
         }
         __syncwarp();
         return slot_buf + 2048 * turn;
     };
     // One unit of 32 output columns: sub-tile `sub`, columns c.. of it.
-    auto unit = [&](uint32_t acc, int sub, int c, int m0, int n0, float rs) {
+    auto unit = [&](const Product &pr, const CUtensorMap *out, uint32_t acc, int sub, int c, int m0, int n0, float rs) {
         const int n = n0 + sub * (EPI == EPI_GATE ? half : W) + c;   // output column
         const long long m = m0 + lane;
-        const bool in = m0 < p.M && n < p.N;
+        const bool in = m0 < pr.M && n < pr.N;
         const int col = sub * GT_W + c;
         float v[32];
         uint8_t *buf;
         if constexpr (EPI == EPI_STORE) {
             get(acc, col, v);
             if constexpr (S8) {
-                apply_scale(v, rs, p.col_scale0, n, p.N);
+                apply_scale(v, rs, p.col_scale0, n, pr.N);
                 if (p.bias)
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] += n + i < p.N ? __ldg(p.bias + n + i) : 0.f;
+                    for (int i = 0; i < 32; ++i) v[i] += n + i < pr.N ? __ldg(p.bias + n + i) : 0.f;
             }
             buf = acquire();
-            if (p.out_dtype == MOE_FP32) stage32(buf, lane, v);
-            else stage16(buf, lane, v, p.out_dtype == MOE_FP16);
+            if (pr.out_dtype == MOE_FP32) stage32(buf, lane, v);
+            else stage16(buf, lane, v, pr.out_dtype == MOE_FP16);
         } else if constexpr (EPI == EPI_GATE) {
             float u[32];
             get(acc, col, v);
             get(acc, col + half, u);
             if constexpr (S8) {
-                apply_scale(v, rs, p.col_scale0, n, p.N);
-                apply_scale(u, rs, p.col_scale1, n, p.N);
+                apply_scale(v, rs, p.col_scale0, n, pr.N);
+                apply_scale(u, rs, p.col_scale1, n, pr.N);
             }
             buf = acquire();
             if constexpr (!S8)
@@ -403,13 +465,13 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
             if constexpr (S8) stage32(buf, lane, v);   // h in fp32, for the quantisation that follows
             else stage16(buf, lane, v, p.fp16);
         } else {
-            const uint4 *gp = reinterpret_cast<const uint4 *>((const uint16_t *)p.in1 + m * p.N + n);
-            const uint4 *up = reinterpret_cast<const uint4 *>((const uint16_t *)p.in2 + m * p.N + n);
+            const uint4 *gp = reinterpret_cast<const uint4 *>((const uint16_t *)p.in1 + m * pr.N + n);
+            const uint4 *up = reinterpret_cast<const uint4 *>((const uint16_t *)p.in2 + m * pr.N + n);
             uint4 gw[4], uw[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 gw[j] = uw[j] = make_uint4(0, 0, 0, 0);
-                if (m < p.M && n + 8 * j < p.N) gw[j] = gp[j], uw[j] = up[j];   // N is a multiple of 8
+                if (m < pr.M && n + 8 * j < pr.N) gw[j] = gp[j], uw[j] = up[j];   // N is a multiple of 8
             }
             get(acc, col, v);
             buf = acquire();
@@ -432,33 +494,33 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
         fence_async_smem();
         __syncwarp();
         if (lane == 0 && in) {
-            if (EPI == EPI_STORE && p.add) tma_add(&maps.out[0], n, m0, buf);
-            else tma_store(&maps.out[0], n, m0, buf);
-            if (EPI == EPI_GATE_BWD || (EPI == EPI_GATE && !S8 && p.extra)) tma_store(&maps.out[1], n, m0, buf + 2048);
-            if (EPI != EPI_STORE && !S8 && p.extra) tma_store(&maps.out[2], n, m0, buf + 4096);
+            if (EPI == EPI_STORE && pr.add) tma_add(out, n, m0, buf);
+            else tma_store(out, n, m0, buf);
+            if (EPI == EPI_GATE_BWD || (EPI == EPI_GATE && !S8 && p.extra)) tma_store(out + 1, n, m0, buf + 2048);
+            if (EPI != EPI_STORE && !S8 && p.extra) tma_store(out + 2, n, m0, buf + 4096);
             tma_commit();
         }
-        if (rotate && in) turn = turn == 2 ? 0 : turn + 1;
+        if (p.rotate && in) turn = turn == 2 ? 0 : turn + 1;
     };
 
     const int sub_units = (EPI == EPI_GATE ? half : W) / GT_UNIT;
     if (p.splits == 1) {
         if (warp >= GT_EPI_W0) {
             const uint32_t empty0 = CG == 2 ? map_rank(&bar->acc_empty[0], even) : su32(&bar->acc_empty[0]);
-            int n = 0;
-            for (int t = first; t < n_tiles; t += step, ++n) {
+            for (int n = 0, t; (t = order.at(n)) >= 0; ++n) {
                 int m0, n0;
-                tile_at(t, m0, n0);
+                const int g = tile_at(t, m0, n0);
+                const Product &pr = p.prod[g];
                 m0 += rank * 128 + 32 * q;                    // this warp's 32 rows
                 float rs = 1.f;
-                if constexpr (S8) rs = m0 + lane < p.M ? p.row_scale[m0 + lane] : 0.f;
+                if constexpr (S8) rs = m0 + lane < pr.M ? p.row_scale[m0 + lane] : 0.f;
                 const int slot = two_acc ? n & 1 : 0, use = two_acc ? n >> 1 : n;
                 if (!mbar_wait(&bar->acc_full[slot], use & 1)) break;
                 tc_fence_after();
                 const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + GT_W * slot;
 #pragma unroll 1
                 for (int u = team; u < sub_units * p.subs; u += 2)
-                    unit(acc, u / sub_units, GT_UNIT * (u % sub_units), m0, n0, rs);
+                    unit(pr, &maps.out[g], acc, u / sub_units, GT_UNIT * (u % sub_units), m0, n0, rs);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(empty0 + 8 * slot);   // the accumulators may be overwritten
@@ -468,7 +530,8 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
         // one tile per cluster: every split leaves its accumulators in shared memory (16 bytes, four columns, a row; the
         // ring is free once the last MMA has completed), and the splits share out the units
         int m0, n0;
-        tile_at(first, m0, n0);
+        const int g = tile_at(order.at(0), m0, n0);
+        const Product &pr = p.prod[g];
         m0 += rank * 128 + 32 * q;
         if (warp >= GT_EPI_W0 && mbar_wait(&bar->acc_full[0], 0)) {
             tc_fence_after();
@@ -485,9 +548,9 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
         cluster_sync();
         if (warp >= GT_EPI_W0) {
             float rs = 1.f;
-            if constexpr (S8) rs = m0 + lane < p.M ? p.row_scale[m0 + lane] : 0.f;
+            if constexpr (S8) rs = m0 + lane < pr.M ? p.row_scale[m0 + lane] : 0.f;
             for (int u = split + p.splits * team; u < sub_units * p.subs; u += 2 * p.splits)
-                unit(0, u / sub_units, GT_UNIT * (u % sub_units), m0, n0, rs);
+                unit(pr, &maps.out[g], 0, u / sub_units, GT_UNIT * (u % sub_units), m0, n0, rs);
         }
     }
     if (warp >= GT_EPI_W0 && lane == 0) tma_wait_read<0>();   // the stores have read shared memory; the grid's end completes them
@@ -540,9 +603,9 @@ int current_device(int *dev) {
     return *dev < kMaxDevices ? MOE_OK : set_error(MOE_ERR_UNSUPPORTED, "device index above 63");
 }
 
-template <bool S8, bool A_MN, bool B_MN, int EPI, int CG>
-int launch_tc(const Maps &maps, const TileArgs &p, int clusters, cudaStream_t st) {
-    auto kern = k_gemm_tc<S8, A_MN, B_MN, EPI, CG>;
+template <bool S8, int A_MN, bool B_MN, int EPI, int CG, int NG>
+int launch_tc(const Maps<NG> &maps, const TileArgs<NG> &p, int clusters, cudaStream_t st) {
+    auto kern = k_gemm_tc<S8, A_MN, B_MN, EPI, CG, NG>;
     static int ready[kMaxDevices] = {};   // this kernel's shared-memory limit is set on the device
     int dev = 0;
     QE_TRY(current_device(&dev));
@@ -575,7 +638,7 @@ int active_clusters(int size, int *out) {
     QE_TRY(current_device(&dev));
     int n = __atomic_load_n(&known[dev][size], __ATOMIC_RELAXED);
     if (n == 0) {
-        auto kern = k_gemm_tc<false, false, false, EPI_STORE, 1>;   // every variant has this kernel's needs
+        auto kern = k_gemm_tc<false, 0, false, EPI_STORE, 1, 1>;   // every variant has this kernel's needs
         QE_CHECK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GT_SMEM));
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute at[1];
@@ -601,13 +664,20 @@ struct Shape {
 // Rows of B that a CTA loads for a sub-tile: whole chunks of 64 where the row index is contiguous.
 int b_rows(bool b_mn, int W, int cg) { return b_mn ? (W / cg + 63) / 64 * 64 : W / cg; }
 
+// k steps of all segments.
+int k_steps(const GemmArgs &g) {
+    const int bk = g.type == DT_S8 ? 128 : 64;
+    return (g.K + bk - 1) / bk * g.segs;
+}
+
 // The tile shape with the least modelled time, in SM cycles.  A k step takes the longer of its MMAs (2 cycles a column:
 // 128 rows x 64 values x 1 column at 4096 multiply-adds a cycle) and its loads (72 bytes a cycle from L2 to an SM); a
 // tile's epilogue 2700 cycles and 14.5 a column (the gate's gradient, with its loads, 3.7 times that), hidden behind the
 // next tile where there is one; a split adds the exchange, 2000 cycles, 24.5 a column and 356 a CTA of the cluster; a
 // pair 1250 to start.  Fitted to 2,700 timings of 85 products (40 to 2,200 rows) on B200: the chosen shape is on average
 // 1.5 % and at most 17 % slower than the fastest one.
-int choose(const GemmArgs &g, int ksteps, Shape *best) {
+int choose(const GemmArgs &g, Shape *best, long long *time) {
+    const int ksteps = k_steps(g);
     long long least = -1;
     for (int cg = g.M > 128 ? 2 : 1; cg >= 1; --cg) {
         const int tiles_m = (g.M + 128 * cg - 1) / (128 * cg), a_rows = g.a_mn ? 128 : std::min(g.M, 128);
@@ -638,19 +708,91 @@ int choose(const GemmArgs &g, int ksteps, Shape *best) {
             }
         }
     }
+    *time = least;
+    return MOE_OK;
+}
+
+constexpr long long kLaunchCycles = 10300;   // a launch's own, in the models
+
+// The same for products in one launch (16-bit, B's row index contiguous, stored plainly; pairs, one sub-tile), and the
+// order of its tiles.  `big`: the first one's reduction is longer and its tiles go first.  Back to back, a k step takes
+// 1.18 times the above (shared memory serves the MMAs' reads and the copies' writes) and a tile 1600 cycles more.
+int choose_group(const GemmArgs *g, int n, bool big, Shape *best, int *rounds, long long *time) {
+    long long least = -1;
+    int room = 0;
+    QE_TRY(active_clusters(2, &room));
+    for (int W = 64; W <= GT_W; W += 64) {
+        const long long step = std::max(2 * W, (128 + b_rows(true, W, 2)) * GT_KB / 72), epi = 1800 + W * 29 / 2;
+        long long t_big = 0, t_small = 0, n_big = 0, n_small = 0;
+        for (int i = 0; i < n; ++i) {
+            const long long tiles = (long long)((g[i].M + 255) / 256) * ((g[i].N + W - 1) / W);
+            const long long t = std::max(k_steps(g[i]) * step * 118 / 100 + 1600, epi);
+            if (big && i == 0) t_big = t, n_big = tiles;
+            else t_small = t, n_small += tiles;
+        }
+        const long long over = n_big % room, rest = room - over;   // clusters with and without one more big tile
+        for (long long r = 0; r <= (over ? n_small / rest : 0); ++r) {
+            const long long after = (n_small - r * rest + room - 1) / room;
+            const long long t = 1250 + epi + n_big / room * t_big + std::max((over ? t_big : 0) + after * t_small, (r + after) * t_small);
+            if (least < 0 || t < least) {
+                least = t;
+                *best = {2, W, 1, 1};
+                *rounds = (int)r;
+            }
+        }
+    }
+    *time = least;
     return MOE_OK;
 }
 
 template <int CG>
-int dispatch(const GemmArgs &g, const Maps &m, const TileArgs &p, int clusters, cudaStream_t st) {
+int dispatch(const GemmArgs &g, const Maps<1> &m, const TileArgs<1> &p, int clusters, cudaStream_t st) {
     if (g.type == DT_S8)
-        return g.epi == EPI_GATE ? launch_tc<true, false, false, EPI_GATE, CG>(m, p, clusters, st)
-                                 : launch_tc<true, false, false, EPI_STORE, CG>(m, p, clusters, st);
-    if (g.epi == EPI_GATE) return launch_tc<false, false, false, EPI_GATE, CG>(m, p, clusters, st);
-    if (g.epi == EPI_GATE_BWD) return launch_tc<false, false, true, EPI_GATE_BWD, CG>(m, p, clusters, st);
-    if (g.a_mn) return launch_tc<false, true, true, EPI_STORE, CG>(m, p, clusters, st);
-    if (g.b_mn) return launch_tc<false, false, true, EPI_STORE, CG>(m, p, clusters, st);
-    return launch_tc<false, false, false, EPI_STORE, CG>(m, p, clusters, st);
+        return g.epi == EPI_GATE ? launch_tc<true, 0, false, EPI_GATE, CG, 1>(m, p, clusters, st)
+                                 : launch_tc<true, 0, false, EPI_STORE, CG, 1>(m, p, clusters, st);
+    if (g.epi == EPI_GATE) return launch_tc<false, 0, false, EPI_GATE, CG, 1>(m, p, clusters, st);
+    if (g.epi == EPI_GATE_BWD) return launch_tc<false, 0, true, EPI_GATE_BWD, CG, 1>(m, p, clusters, st);
+    if (g.b_mn) return launch_tc<false, 0, true, EPI_STORE, CG, 1>(m, p, clusters, st);
+    return launch_tc<false, 0, false, EPI_STORE, CG, 1>(m, p, clusters, st);
+}
+
+// Product i of a launch: its sizes and descriptors.
+template <int NG>
+int set_product(const GemmArgs &g, int i, const Shape &sh, Maps<NG> &m, TileArgs<NG> &p) {
+    const int bk = g.type == DT_S8 ? 128 : 64, half = sh.W / 2, tm = 128 * sh.cg;
+    const int tn = (g.epi == EPI_GATE ? half : sh.W) * sh.subs;
+    Product &pr = p.prod[i];
+    pr.M = g.M, pr.N = g.N, pr.segs = g.segs;
+    pr.kblocks = (g.K + bk - 1) / bk;
+    pr.tiles_m = (g.M + tm - 1) / tm;
+    pr.tiles_n = (g.N + tn - 1) / tn;
+    pr.start = p.tiles;
+    p.tiles += pr.tiles_m * pr.tiles_n;
+    pr.a_mn = g.a_mn;
+    pr.a_rows = sh.cg == 1 && pr.tiles_m == 1 ? (g.M + 7) / 8 * 8 : 128;   // whole 8-row swizzle groups
+    pr.b_ready = g.b_ready;
+    pr.out_dtype = g.out_dtype;
+    pr.add = g.add;
+    const int na = g.segs, nb = g.epi == EPI_GATE ? 2 : g.segs;
+    for (int s = 0; s < na; ++s) {
+        if (g.a_mn) QE_TRY(encode(&m.a[i][s], g.type, g.a[s], g.M, g.K, g.lda, 64, bk));
+        else QE_TRY(encode(&m.a[i][s], g.type, g.a[s], g.K, g.M, g.lda, bk, pr.a_rows));
+    }
+    for (int s = 0; s < nb; ++s) {
+        if (g.b_mn) QE_TRY(encode(&m.b[i][s], g.type, g.b[s], g.N, g.K, g.ldb, 64, bk));
+        else QE_TRY(encode(&m.b[i][s], g.type, g.b[s], g.K, g.N, g.ldb, bk, half));
+    }
+    return encode(&m.out[i], g.out_dtype, g.out, g.N, g.M, g.ldo, GT_UNIT, 32);
+}
+
+template <int NG>
+void set_shape(const GemmArgs &g, const Shape &sh, int ksteps, TileArgs<NG> &p) {
+    p.W = sh.W, p.subs = sh.subs, p.splits = sh.splits;
+    p.kper = (ksteps + sh.splits - 1) / sh.splits;
+    p.b_bytes = b_rows(g.b_mn, sh.W, sh.cg) * GT_KB;
+    p.stage_bytes = GT_A + sh.subs * p.b_bytes;
+    p.stages = std::min(GT_MAX_STAGES, GT_RING / p.stage_bytes);
+    p.fp16 = g.type == MOE_FP16;
 }
 
 }  // namespace
@@ -662,57 +804,74 @@ int read_dense_error(int *code) {
     return MOE_OK;
 }
 
-static int launch_shape(const GemmArgs &g, const Shape &sh, bool b_ready, cudaStream_t st) {
-    const int bk = g.type == DT_S8 ? 128 : 64;
-    Maps m;
-    TileArgs p = {};
-    p.M = g.M, p.N = g.N, p.segs = g.segs;
-    p.kblocks = (g.K + bk - 1) / bk;
-    const int cg = sh.cg, tm = 128 * cg, half = sh.W / 2;
-    const int tn = (g.epi == EPI_GATE ? half : sh.W) * sh.subs;
-    p.tiles_m = (g.M + tm - 1) / tm;
-    p.tiles_n = (g.N + tn - 1) / tn;
-    p.W = sh.W, p.subs = sh.subs, p.splits = sh.splits;
-    p.kper = (p.kblocks * g.segs + sh.splits - 1) / sh.splits;
-    p.b_bytes = b_rows(g.b_mn, sh.W, cg) * GT_KB;
-    p.stage_bytes = GT_A + sh.subs * p.b_bytes;
-    p.stages = std::min(GT_MAX_STAGES, GT_RING / p.stage_bytes);
-    p.a_rows = cg == 1 && p.tiles_m == 1 ? (g.M + 7) / 8 * 8 : 128;   // whole 8-row swizzle groups
-    p.b_ready = b_ready;
+static int launch_shape(const GemmArgs &g, const Shape &sh, cudaStream_t st) {
+    Maps<1> m;
+    TileArgs<1> p = {};
+    QE_TRY(set_product(g, 0, sh, m, p));
+    p.products = 1;
+    set_shape(g, sh, k_steps(g), p);
     p.act = g.act;
-    p.fp16 = g.type == MOE_FP16;
-    p.out_dtype = g.out_dtype;
-    p.add = g.add;
     p.extra = g.out2 != nullptr;
+    p.rotate = g.out_dtype != MOE_FP32 && (g.epi == EPI_STORE || (g.epi == EPI_GATE && !p.extra));
     p.in1 = g.in1, p.in2 = g.in2;
     p.row_scale = g.row_scale, p.col_scale0 = g.col_scale[0], p.col_scale1 = g.col_scale[1], p.bias = g.bias;
-    const int na = g.segs, nb = g.epi == EPI_GATE ? 2 : g.segs;
-    for (int s = 0; s < na; ++s) {
-        if (g.a_mn) QE_TRY(encode(&m.a[s], g.type, g.a[s], g.M, g.K, g.lda, 64, bk));
-        else QE_TRY(encode(&m.a[s], g.type, g.a[s], g.K, g.M, g.lda, bk, p.a_rows));
-    }
-    for (int s = 0; s < nb; ++s) {
-        if (g.b_mn) QE_TRY(encode(&m.b[s], g.type, g.b[s], g.N, g.K, g.ldb, 64, bk));
-        else QE_TRY(encode(&m.b[s], g.type, g.b[s], g.K, g.N, g.ldb, bk, half));
-    }
-    QE_TRY(encode(&m.out[0], g.out_dtype, g.out, g.N, g.M, g.ldo, GT_UNIT, 32));
     if (g.out1) QE_TRY(encode(&m.out[1], g.type, g.out1, g.N, g.M, g.N, GT_UNIT, 32));
     if (g.out2) QE_TRY(encode(&m.out[2], g.type, g.out2, g.N, g.M, g.N, GT_UNIT, 32));
-    const int tiles = p.tiles_m * p.tiles_n;
-    int clusters = tiles;
+    int clusters = p.tiles;
     if (p.splits == 1) {
-        QE_TRY(active_clusters(cg, &clusters));
-        clusters = std::min(clusters, tiles);
+        QE_TRY(active_clusters(sh.cg, &clusters));
+        clusters = std::min(clusters, p.tiles);
     }
-    return cg == 2 ? dispatch<2>(g, m, p, clusters, st) : dispatch<1>(g, m, p, clusters, st);
+    return sh.cg == 2 ? dispatch<2>(g, m, p, clusters, st) : dispatch<1>(g, m, p, clusters, st);
 }
 
-int launch_gemm(const GemmArgs &g, Link link, cudaStream_t st) {
-    if (rows_fit(g)) return launch_rows(g, link, st);
-    const int bk = g.type == DT_S8 ? 128 : 64;
+int launch_gemm(const GemmArgs &g, cudaStream_t st) {
+    if (rows_fit(g)) return launch_rows(g, st);
     Shape sh = {};
-    QE_TRY(choose(g, (g.K + bk - 1) / bk * g.segs, &sh));
-    return launch_shape(g, sh, link.b_ready, st);
+    long long time = 0;
+    QE_TRY(choose(g, &sh, &time));
+    return launch_shape(g, sh, st);
+}
+
+static int launch_group(const GemmArgs *g, int n, bool big, const Shape &sh, int rounds, cudaStream_t st) {
+    Maps<kGroup> m;
+    TileArgs<kGroup> p = {};
+    int longest = 0;
+    p.rotate = 1;
+    for (int i = 0; i < n; ++i) {
+        QE_TRY(set_product(g[i], i, sh, m, p));
+        longest = std::max(longest, k_steps(g[i]));
+        if (g[i].out_dtype == MOE_FP32) p.rotate = 0;
+        if (big && i == 0) p.big = p.tiles;
+    }
+    p.products = n;
+    p.rounds = rounds;
+    set_shape(g[0], sh, longest, p);
+    int clusters = 0;
+    QE_TRY(active_clusters(sh.cg, &clusters));
+    return launch_tc<false, 2, true, EPI_STORE, 2, kGroup>(m, p, std::min(clusters, p.tiles), st);
+}
+
+int launch_gradients(const GemmArgs *dx, const GemmArgs *dw, int n_dw, cudaStream_t st) {
+    GemmArgs all[kGroup];
+    Shape sh = {}, sh_x = {}, sh_w = {};
+    int rounds = 0, rounds_w = 0;
+    long long t_all = 0, t_x = 0, t_w = 0;
+    if (n_dw == 0) return dx ? launch_gemm(*dx, st) : MOE_OK;
+    QE_TRY(choose_group(dw, n_dw, false, &sh_w, &rounds_w, &t_w));
+    if (dx) {
+        all[0] = *dx;
+        for (int i = 0; i < n_dw; ++i) all[1 + i] = dw[i];
+        QE_TRY(choose_group(all, 1 + n_dw, true, &sh, &rounds, &t_all));
+        QE_TRY(choose(*dx, &sh_x, &t_x));
+        // one launch where that is modelled at least 5 % faster: its clusters with a tile of dx less take more of the
+        // others.  Measured on B200: 1001 rows of 2560 x 5120 80 us (two launches 107), 300 rows 58 (68), 4096 rows of
+        // 2048 x 4096 180 (203); but 600 rows of 1024 x 4096 36 (34), where dx alone splits its reduction.
+        if (100 * (t_all + kLaunchCycles) <= 95 * (t_x + t_w + 2 * kLaunchCycles))
+            return launch_group(all, 1 + n_dw, true, sh, rounds, st);
+        QE_TRY(launch_shape(*dx, sh_x, st));
+    }
+    return launch_group(dw, n_dw, false, sh_w, rounds_w, st);
 }
 
 }  // namespace qeffn

@@ -215,7 +215,7 @@ bool rows_fit(const GemmArgs &g) {
     return g.M <= 16 || (g.M <= 32 && bytes <= 24LL << 20);
 }
 
-int launch_rows(const GemmArgs &g, Link link, cudaStream_t st) {
+int launch_rows(const GemmArgs &g, cudaStream_t st) {
     const int size = g.type == DT_S8 ? 1 : 2;
     RowsArgs p = {};
     p.w0 = (const uint8_t *)g.b[0], p.w1 = (const uint8_t *)g.b[1];
@@ -225,7 +225,7 @@ int launch_rows(const GemmArgs &g, Link link, cudaStream_t st) {
     p.act = g.act;
     p.out = g.out, p.out1 = g.out1, p.out2 = g.out2, p.out_dtype = g.out_dtype, p.type = g.type, p.ldo = g.ldo;
     p.row_scale = g.row_scale, p.col_scale0 = g.col_scale[0], p.col_scale1 = g.col_scale[1], p.bias = g.bias;
-    p.first = !link.b_ready;
+    p.first = !g.b_ready;
     const bool gate = g.epi == EPI_GATE;
     if (g.type == DT_S8) return launch_rows_type<DT_S8>(p, gate, st);
     return g.type == MOE_FP16 ? launch_rows_type<MOE_FP16>(p, gate, st) : launch_rows_type<MOE_BF16>(p, gate, st);

@@ -299,8 +299,8 @@ def test_backward(T, d, I, dt):
         check_backward(x, g, u, dy, wg, wu, wd, act, out)
         again = _backward(f, x, g, u, dy)
         assert all(torch.equal(p, q) for p, q in zip(out, again))
-        only_dx = _backward(f, x, g, u, dy, dw=False)
-        assert torch.equal(only_dx[0], out[0])
+        # dx alone may split its reduction, and then sums in another order
+        check_backward(x, g, u, dy, wg, wu, wd, act, _backward(f, x, g, u, dy, dw=False))
         only_dw = _backward(f, x, g, u, dy, dx=False)
         assert all(torch.equal(p, q) for p, q in zip(only_dw[1:], out[1:]))
     assert capi.moe_ffn_get_device_error() == 0
