@@ -36,10 +36,10 @@ constexpr int GT_W = 256;                   // largest sub-tile width; TMEM colu
 constexpr int GT_KB = 128;                  // bytes of the reduction index per stage
 constexpr int GT_A = 128 * GT_KB;           // bytes of A per stage: 128 rows of one k step
 constexpr int GT_MAX_STAGES = 8;
-constexpr int GT_RING = 177 * 1024;         // bytes of the stage ring
+constexpr int GT_RING = 161 * 1024;         // bytes of the stage ring
 constexpr int GT_EPI_W0 = 4, GT_EPI_NW = 8;
 constexpr int GT_UNIT = 32;                 // columns an epilogue warp handles at a time
-constexpr int GT_SLOT = 6144;               // an epilogue warp's store tiles: three of 32 rows x 64 bytes (one of fp32)
+constexpr int GT_SLOT = 8192;               // an epilogue warp's store tiles: two of 32 rows x 128 bytes, or three x 64
 constexpr int GT_SMEM = 1024 + GT_RING + GT_EPI_NW * GT_SLOT + 256;
 
 // A launch is one product, or a group of up to four that share the tile shape (the gradients).
@@ -67,7 +67,8 @@ struct TileArgs {
     int stages, stage_bytes, b_bytes;   // b_bytes: a sub-tile's B in one CTA
     int act;
     int fp16;                   // 16-bit operands (and out1, out2): fp16 rather than bf16
-    int rotate;                 // 16-bit outputs throughout, one a tile: the store tiles take turns
+    int one_out;                // one output a tile: two store tiles take turns
+    int wide;                   // it is 16-bit and its store tiles have 64 columns
     int extra;                  // out1 and out2 wanted (EPI_GATE: both, EPI_GATE_BWD: out2)
     const void *in1, *in2;
     const float *row_scale, *col_scale0, *col_scale1, *bias;
@@ -120,14 +121,15 @@ __device__ __forceinline__ float2 unpack16(uint32_t v, int fp16) {
     return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162 *>(&v));
 }
 
-// 32 values of this lane's row into a 32 x 32 store tile of 64-byte rows (64-byte swizzle: 16-byte part c of row r at
-// part c ^ (r / 2 % 4)).
-__device__ __forceinline__ void stage16(uint8_t *buf, int lane, const float (&v)[32], int fp16) {
+// 32 values of this lane's row into a store tile of 32 rows: of 64 bytes (64-byte swizzle: 16-byte part c of row r at part
+// c ^ (r / 2 % 4)), or half h of 128 bytes (128-byte swizzle: part c at c ^ (r % 8)).
+__device__ __forceinline__ void stage16(uint8_t *buf, int lane, const float (&v)[32], int fp16, bool wide = false, int h = 0) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         const uint4 w = make_uint4(pack16(v[8 * c], v[8 * c + 1], fp16), pack16(v[8 * c + 2], v[8 * c + 3], fp16),
                                    pack16(v[8 * c + 4], v[8 * c + 5], fp16), pack16(v[8 * c + 6], v[8 * c + 7], fp16));
-        *reinterpret_cast<uint4 *>(buf + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = w;
+        const int at = wide ? lane * 128 + (((4 * h + c) ^ (lane & 7)) << 4) : lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4);
+        *reinterpret_cast<uint4 *>(buf + at) = w;
     }
 }
 // 32 fp32 values: the whole 128-byte row (128-byte swizzle).
@@ -418,52 +420,61 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
                 for (int i = 0; i < 32; ++i) v[i] = (float)sum[i];
         }
     };
-    // Store tiles: three 16-bit ones in turn where a unit has one output, else all at once.
+    // Store tiles: two in turn where a tile has one output, else all at once.
     int turn = 0;
     auto acquire = [&]() {
         if (lane == 0) {
-            if (p.rotate) tma_wait_read<2>();
+            if (p.one_out) tma_wait_read<1>();
             else tma_wait_read<0>();
         }
         __syncwarp();
-        return slot_buf + 2048 * turn;
+        return slot_buf + 4096 * turn;
     };
-    // One unit of 32 output columns: sub-tile `sub`, columns c.. of it.
+    const bool wide = (EPI == EPI_STORE || (EPI == EPI_GATE && !S8)) && p.wide;
+    const int unit_cols = wide ? 2 * GT_UNIT : GT_UNIT;
+    // One unit of 32 (wide: 64) output columns: sub-tile `sub`, columns c.. of it.
     auto unit = [&](const Product &pr, const CUtensorMap *out, uint32_t acc, int sub, int c, int m0, int n0, float rs) {
         const int n = n0 + sub * (EPI == EPI_GATE ? half : W) + c;   // output column
         const long long m = m0 + lane;
         const bool in = m0 < pr.M && n < pr.N;
         const int col = sub * GT_W + c;
         float v[32];
-        uint8_t *buf;
+        uint8_t *buf = nullptr;
         if constexpr (EPI == EPI_STORE) {
-            get(acc, col, v);
-            if constexpr (S8) {
-                apply_scale(v, rs, p.col_scale0, n, pr.N);
-                if (p.bias)
+#pragma unroll 1
+            for (int h = 0; h <= (int)wide; ++h) {
+                const int nh = n + 32 * h;
+                get(acc, col + 32 * h, v);
+                if constexpr (S8) {
+                    apply_scale(v, rs, p.col_scale0, nh, pr.N);
+                    if (p.bias)
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] += n + i < pr.N ? __ldg(p.bias + n + i) : 0.f;
-            }
-            buf = acquire();
-            if (pr.out_dtype == MOE_FP32) stage32(buf, lane, v);
-            else stage16(buf, lane, v, pr.out_dtype == MOE_FP16);
-        } else if constexpr (EPI == EPI_GATE) {
-            float u[32];
-            get(acc, col, v);
-            get(acc, col + half, u);
-            if constexpr (S8) {
-                apply_scale(v, rs, p.col_scale0, n, pr.N);
-                apply_scale(u, rs, p.col_scale1, n, pr.N);
-            }
-            buf = acquire();
-            if constexpr (!S8)
-                if (p.extra) {
-                    stage16(buf + 2048, lane, v, p.fp16);
-                    stage16(buf + 4096, lane, u, p.fp16);
+                        for (int i = 0; i < 32; ++i) v[i] += nh + i < pr.N ? __ldg(p.bias + nh + i) : 0.f;
                 }
-            gate_all(p.act, v, u);
-            if constexpr (S8) stage32(buf, lane, v);   // h in fp32, for the quantisation that follows
-            else stage16(buf, lane, v, p.fp16);
+                if (h == 0) buf = acquire();
+                if (pr.out_dtype == MOE_FP32) stage32(buf, lane, v);
+                else stage16(buf, lane, v, pr.out_dtype == MOE_FP16, wide, h);
+            }
+        } else if constexpr (EPI == EPI_GATE) {
+#pragma unroll 1
+            for (int h = 0; h <= (int)wide; ++h) {
+                float u[32];
+                get(acc, col + 32 * h, v);
+                get(acc, col + half + 32 * h, u);
+                if constexpr (S8) {
+                    apply_scale(v, rs, p.col_scale0, n, pr.N);
+                    apply_scale(u, rs, p.col_scale1, n, pr.N);
+                }
+                if (h == 0) buf = acquire();
+                if constexpr (!S8)
+                    if (p.extra) {
+                        stage16(buf + 2048, lane, v, p.fp16);
+                        stage16(buf + 4096, lane, u, p.fp16);
+                    }
+                gate_all(p.act, v, u);
+                if constexpr (S8) stage32(buf, lane, v);   // h in fp32, for the quantisation that follows
+                else stage16(buf, lane, v, p.fp16, wide, h);
+            }
         } else {
             const uint4 *gp = reinterpret_cast<const uint4 *>((const uint16_t *)p.in1 + m * pr.N + n);
             const uint4 *up = reinterpret_cast<const uint4 *>((const uint16_t *)p.in2 + m * pr.N + n);
@@ -500,10 +511,10 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
             if (EPI != EPI_STORE && !S8 && p.extra) tma_store(out + 2, n, m0, buf + 4096);
             tma_commit();
         }
-        if (p.rotate && in) turn = turn == 2 ? 0 : turn + 1;
+        if (p.one_out && in) turn ^= 1;
     };
 
-    const int sub_units = (EPI == EPI_GATE ? half : W) / GT_UNIT;
+    const int sub_units = (EPI == EPI_GATE ? half : W) / unit_cols;
     if (p.splits == 1) {
         if (warp >= GT_EPI_W0) {
             const uint32_t empty0 = CG == 2 ? map_rank(&bar->acc_empty[0], even) : su32(&bar->acc_empty[0]);
@@ -520,7 +531,7 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
                 const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + GT_W * slot;
 #pragma unroll 1
                 for (int u = team; u < sub_units * p.subs; u += 2)
-                    unit(pr, &maps.out[g], acc, u / sub_units, GT_UNIT * (u % sub_units), m0, n0, rs);
+                    unit(pr, &maps.out[g], acc, u / sub_units, unit_cols * (u % sub_units), m0, n0, rs);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(empty0 + 8 * slot);   // the accumulators may be overwritten
@@ -550,7 +561,7 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
             float rs = 1.f;
             if constexpr (S8) rs = m0 + lane < pr.M ? p.row_scale[m0 + lane] : 0.f;
             for (int u = split + p.splits * team; u < sub_units * p.subs; u += 2 * p.splits)
-                unit(pr, &maps.out[g], 0, u / sub_units, GT_UNIT * (u % sub_units), m0, n0, rs);
+                unit(pr, &maps.out[g], 0, u / sub_units, unit_cols * (u % sub_units), m0, n0, rs);
         }
     }
     if (warp >= GT_EPI_W0 && lane == 0) tma_wait_read<0>();   // the stores have read shared memory; the grid's end completes them
@@ -671,11 +682,13 @@ int k_steps(const GemmArgs &g) {
 }
 
 // The tile shape with the least modelled time, in SM cycles.  A k step takes the longer of its MMAs (2 cycles a column:
-// 128 rows x 64 values x 1 column at 4096 multiply-adds a cycle) and its loads (72 bytes a cycle from L2 to an SM); a
-// tile's epilogue 2700 cycles and 14.5 a column (the gate's gradient, with its loads, 3.7 times that), hidden behind the
+// 128 rows x 64 values x 1 column at 4096 multiply-adds a cycle), its loads (72 bytes a cycle from L2 to an SM) and its
+// shared-memory traffic (the copies' writes and the MMAs' reads, 0.9 cycles a 128-byte row); narrow sub-tiles are counted
+// an eighth slower in long launches, where the power that their extra traffic takes lowers the clock (4096 x 4096 x 8192:
+// W = 192 229 us, 256 189 us, though equal on zeros, which take no power); a tile's epilogue 2700 cycles and 14.5 a column (the gate's gradient, with its loads, 3.7 times that), hidden behind the
 // next tile where there is one; a split adds the exchange, 2000 cycles, 24.5 a column and 356 a CTA of the cluster; a
 // pair 1250 to start.  Fitted to 2,700 timings of 85 products (40 to 2,200 rows) on B200: the chosen shape is on average
-// 1.5 % and at most 17 % slower than the fastest one.
+// 1.7 % and at most 17 % slower than the fastest one.
 int choose(const GemmArgs &g, Shape *best, long long *time) {
     const int ksteps = k_steps(g);
     long long least = -1;
@@ -693,7 +706,9 @@ int choose(const GemmArgs &g, Shape *best, long long *time) {
                     const int C = W * subs, out = g.epi == EPI_GATE ? C / 2 : C;
                     const int tiles_n = (g.N + out - 1) / out, waves = (int)(((long long)tiles_m * tiles_n + room - 1) / room);
                     if (splits > 1 && C * 512 > GT_RING) break;    // the partial tile has to fit
-                    const int step = std::max(2 * C, (a_rows + subs * b_rows(g.b_mn, W, cg)) * GT_KB / 72);
+                    const int br = b_rows(g.b_mn, W, cg);
+                    int step = std::max(2 * C, std::max((a_rows + subs * br) * GT_KB / 72, 9 * (a_rows * (subs + 1) + 2 * subs * br) / 10));
+                    if (W < GT_W && waves >= 3) step += step / 8;
                     const long long main = (long long)kper * step, epi = 2700 + C * (g.epi == EPI_GATE_BWD ? 54 : 29 / 2);
                     long long t = cg == 2 ? 1250 : 0;
                     if (splits > 1) t += waves * (main + 2000 + 49 * C / 2 + 356 * cg * splits + epi / splits);
@@ -782,7 +797,7 @@ int set_product(const GemmArgs &g, int i, const Shape &sh, Maps<NG> &m, TileArgs
         if (g.b_mn) QE_TRY(encode(&m.b[i][s], g.type, g.b[s], g.N, g.K, g.ldb, 64, bk));
         else QE_TRY(encode(&m.b[i][s], g.type, g.b[s], g.K, g.N, g.ldb, bk, half));
     }
-    return encode(&m.out[i], g.out_dtype, g.out, g.N, g.M, g.ldo, GT_UNIT, 32);
+    return encode(&m.out[i], g.out_dtype, g.out, g.N, g.M, g.ldo, g.out_dtype != MOE_FP32 && p.wide ? 2 * GT_UNIT : GT_UNIT, 32);
 }
 
 template <int NG>
@@ -807,12 +822,13 @@ int read_dense_error(int *code) {
 static int launch_shape(const GemmArgs &g, const Shape &sh, cudaStream_t st) {
     Maps<1> m;
     TileArgs<1> p = {};
+    p.extra = g.out2 != nullptr;
+    p.one_out = g.epi == EPI_STORE || (g.epi == EPI_GATE && !p.extra);
+    p.wide = p.one_out && g.out_dtype != MOE_FP32 && (g.epi == EPI_GATE ? sh.W / 2 : sh.W) % (2 * GT_UNIT) == 0;
     QE_TRY(set_product(g, 0, sh, m, p));
     p.products = 1;
     set_shape(g, sh, k_steps(g), p);
     p.act = g.act;
-    p.extra = g.out2 != nullptr;
-    p.rotate = g.out_dtype != MOE_FP32 && (g.epi == EPI_STORE || (g.epi == EPI_GATE && !p.extra));
     p.in1 = g.in1, p.in2 = g.in2;
     p.row_scale = g.row_scale, p.col_scale0 = g.col_scale[0], p.col_scale1 = g.col_scale[1], p.bias = g.bias;
     if (g.out1) QE_TRY(encode(&m.out[1], g.type, g.out1, g.N, g.M, g.N, GT_UNIT, 32));
@@ -837,11 +853,13 @@ static int launch_group(const GemmArgs *g, int n, bool big, const Shape &sh, int
     Maps<kGroup> m;
     TileArgs<kGroup> p = {};
     int longest = 0;
-    p.rotate = 1;
+    p.one_out = 1;
+    p.wide = 1;
+    for (int i = 0; i < n; ++i)
+        if (g[i].out_dtype == MOE_FP32) p.wide = 0;
     for (int i = 0; i < n; ++i) {
         QE_TRY(set_product(g[i], i, sh, m, p));
         longest = std::max(longest, k_steps(g[i]));
-        if (g[i].out_dtype == MOE_FP32) p.rotate = 0;
         if (big && i == 0) p.big = p.tiles;
     }
     p.products = n;
