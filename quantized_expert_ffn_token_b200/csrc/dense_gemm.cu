@@ -681,14 +681,14 @@ int k_steps(const GemmArgs &g) {
     return (g.K + bk - 1) / bk * g.segs;
 }
 
-// The tile shape with the least modelled time, in SM cycles.  A k step takes the longer of its MMAs (2 cycles a column:
+// The tile shape with the least modelled time, in SM cycles.  A k step takes the longest of its MMAs (2 cycles a column:
 // 128 rows x 64 values x 1 column at 4096 multiply-adds a cycle), its loads (72 bytes a cycle from L2 to an SM) and its
-// shared-memory traffic (the copies' writes and the MMAs' reads, 0.9 cycles a 128-byte row); narrow sub-tiles are counted
-// an eighth slower in long launches, where the power that their extra traffic takes lowers the clock (4096 x 4096 x 8192:
-// W = 192 229 us, 256 189 us, though equal on zeros, which take no power); a tile's epilogue 2700 cycles and 14.5 a column (the gate's gradient, with its loads, 3.7 times that), hidden behind the
-// next tile where there is one; a split adds the exchange, 2000 cycles, 24.5 a column and 356 a CTA of the cluster; a
-// pair 1250 to start.  Fitted to 2,700 timings of 85 products (40 to 2,200 rows) on B200: the chosen shape is on average
-// 1.7 % and at most 17 % slower than the fastest one.
+// shared-memory traffic (the copies' writes and the MMAs' reads, 0.9 cycles a 128-byte row).  Narrow sub-tiles are
+// counted 4 % slower in long launches, where their extra traffic costs clock (4096 x 4096 x 8192 over and over: W = 192
+// 231 us, 256 222 us; one at a time 197 and 195).  A tile's epilogue takes 2700 cycles and 14.5 a column (the gate's
+// gradient, with its loads, 3.7 times that), hidden behind the next tile where there is one; a split adds the exchange,
+// 2000 cycles, 24.5 a column and 356 a CTA of the cluster; a pair 1250 to start.  Fitted to 2,700 timings of 85 products
+// (40 to 2,200 rows) on B200: the chosen shape is on average 1.7 % and at most 17 % slower than the fastest one.
 int choose(const GemmArgs &g, Shape *best, long long *time) {
     const int ksteps = k_steps(g);
     long long least = -1;
@@ -708,7 +708,7 @@ int choose(const GemmArgs &g, Shape *best, long long *time) {
                     if (splits > 1 && C * 512 > GT_RING) break;    // the partial tile has to fit
                     const int br = b_rows(g.b_mn, W, cg);
                     int step = std::max(2 * C, std::max((a_rows + subs * br) * GT_KB / 72, 9 * (a_rows * (subs + 1) + 2 * subs * br) / 10));
-                    if (W < GT_W && waves >= 3) step += step / 8;
+                    if (W < GT_W && waves >= 3) step += step / 25;
                     const long long main = (long long)kper * step, epi = 2700 + C * (g.epi == EPI_GATE_BWD ? 54 : 29 / 2);
                     long long t = cg == 2 ? 1250 : 0;
                     if (splits > 1) t += waves * (main + 2000 + 49 * C / 2 + 356 * cg * splits + epi / splits);
