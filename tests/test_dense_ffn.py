@@ -9,7 +9,9 @@ of n such terms c_k e_k, |e_k| <= u, is a sum of bounded independent errors,
 and exceeds 6 u sqrt(sum c_k^2) with probability below 2 e^-18 (Hoeffding).
 fp32 accumulation adds at most n 2^-24 of the sum of magnitudes; ``U32`` = 2^-19
 of it covers every n used here (at most 2^5 partial sums deep per output in
-any kernel, fast exponential and division within a few 2^-22).
+any kernel).  An activation carries at most ``UACT`` of itself: CUDA documents
+__expf(x) within 2 + 1.17 |x| units in the last place, |x| < 89 where it is not
+zero, i.e. 107 * 2^-23 < 2^-16.
 """
 import ctypes
 
@@ -21,6 +23,7 @@ from quantized_expert_ffn_token_b200 import capi
 
 U = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24}
 U32 = 2.0 ** -19
+UACT = 2.0 ** -16
 ACTS = ["silu", "gelu_tanh", "gelu"]
 
 
@@ -30,8 +33,8 @@ def act64(z, act):
     if act == "silu":
         return z * torch.sigmoid(z)
     if act == "gelu_tanh":
-        return 0.5 * z * (1 + torch.tanh((2 / torch.pi) ** 0.5 * (z + 0.044715 * z ** 3)))
-    return z * torch.special.ndtr(z)
+        return z * torch.sigmoid((8 / torch.pi) ** 0.5 * (z + 0.044715 * z ** 3))   # (1 + tanh v) / 2, exact in the tail
+    return z * 0.5 * torch.special.erfc(-z * 0.5 ** 0.5)                     # exact in the tail
 
 
 def ffn64(x, wg, wu, wd, act):
@@ -225,11 +228,11 @@ def check_forward(x, wg, wu, wd, act, y, g, u):
         check(g, g64, U[dt] * g64.abs() + eg + 1e-7, "gate")
         check(u, u64, U[dt] * u64.abs() + eu + 1e-7, "up")
     # |act'| <= 1.13: errors of the fp32 sums g and u pass into h and on into y
-    eh = 1.13 * eg * u64.abs() + act64(g64, act).abs() * eu + U32 * h64.abs()
+    eh = 1.13 * eg * u64.abs() + act64(g64, act).abs() * eu + UACT * h64.abs()
     tiny = 2.0 ** -24 if dt == torch.float16 else 0.0       # fp16 subnormal spacing of h and y
     check(y, y64, U[dt] * y64.abs() + sum_tol(h64, D, U[dt]) + eh @ D.abs().T + tiny * (1 + D.abs().sum(1)), "y")
-    # roundings of y and of h, one u each in the relative 2-norm
-    assert (y.double() - y64).norm() <= 2 * U[dt] * y64.norm() + tiny * y64.numel()
+    # roundings of y and of h, one u each in the relative 2-norm (on average: with few elements the bound above decides)
+    assert y.numel() < 4096 or (y.double() - y64).norm() <= 2 * U[dt] * y64.norm() + tiny * y64.numel()
 
 
 @pytest.mark.gpu
@@ -269,22 +272,23 @@ def check_backward(x, g, u, dy, wg, wu, wd, act, out, dw_dtype=None, base=0.0):
     dg, du, h = dh * u64 * dact, dh * a, a * u64
     # errors of dg, du before they are rounded: the fp32 sum dh, and a few fp32 steps in act and act', whose
     # terms (at most max(1, |g|) in size where they cancel) are bounded by 2 + |g| e^-|g| < 3 of fp32's
-    edg, edu = edh * (u64 * dact).abs() + 3 * U32 * (dh * u64).abs(), edh * a.abs() + U32 * du.abs()
+    edg, edu = edh * (u64 * dact).abs() + 3 * UACT * (dh * u64).abs(), edh * a.abs() + UACT * du.abs()
     tiny = 2.0 ** -24 if dt == torch.float16 else 0.0
     want = [dg @ G + du @ W, dg.T @ X, du.T @ X, dy64.T @ h]
     tol = [sum_tol(dg, G.T, U[dt]) + sum_tol(du, W.T, U[dt]) + edg @ G.abs() + edu @ W.abs()
            + tiny * (1 + G.abs().sum(0) + W.abs().sum(0)),
            sum_tol(dg.T, X.T, U[dt]) + edg.T @ X.abs() + tiny * (1 + X.abs().sum(0)),
            sum_tol(du.T, X.T, U[dt]) + edu.T @ X.abs() + tiny * (1 + X.abs().sum(0)),
-           sum_tol(h.T, dy64.T, U[dt]).T + U32 * (dy64.abs().T @ h.abs()) + tiny * (1 + dy64.abs().sum(0))[:, None]]
+           sum_tol(h.T, dy64.T, U[dt]).T + UACT * (dy64.abs().T @ h.abs()) + tiny * (1 + dy64.abs().sum(0))[:, None]]
     for i, name in enumerate(("dx", "dw_gate", "dw_up", "dw_down")):
         if out[i] is None:
             continue
         w = want[i] + (base if i else 0.0)
         r = (U[dt] if i == 0 else uo)
         check(out[i], w, r * w.abs() + tol[i] + 1e-30, name)
-        # the output's rounding and the operand's (dx: two operands, independent), one u each
-        assert (out[i].double() - w).norm() <= 2 * U[dt] * w.norm() + tiny * w.numel(), name
+        # the output's rounding and the operand's (dx: two operands, independent), one u each on average: a sum over
+        # few elements can lie anywhere within the bound above
+        assert w.numel() < 4096 or (out[i].double() - w).norm() <= 2 * U[dt] * w.norm() + tiny * w.numel(), name
 
 
 @pytest.mark.gpu
@@ -488,9 +492,11 @@ def check_ffn_s8(x, wq, act, y):
     frac = (h / torch.where(sh > 0, sh, torch.ones_like(sh))[:, None]).abs() % 1
     near = ((frac - 0.5).abs() <= 127 * 2.0 ** -18).double()
     tiny = 2.0 ** -24 if x.dtype == torch.float16 else 0.0
-    tol = mm(near, sh, wd.abs(), sd) + (U[x.dtype] + 2.0 ** -17) * want.abs() + 2.0 ** -18 * mm(qh.abs(), sh, wd.abs(), sd)
+    other = mm(near, sh, wd.abs(), sd) + 2.0 ** -18 * mm(qh.abs(), sh, wd.abs(), sd)
+    # the value that is rounded last is at most |want| + other, and the rounding is relative to it
+    tol = other + (U[x.dtype] + 2.0 ** -17) * (want.abs() + other)
     check(y, want, tol + tiny, "y")
-    assert (y.double() - want).norm() <= 2 * U[x.dtype] * want.norm() + tiny * want.numel()
+    assert y.numel() < 4096 or (y.double() - want).norm() <= 2 * U[x.dtype] * want.norm() + 1.01 * other.norm() + tiny * want.numel()
 
 
 def _quantized(w):
