@@ -108,13 +108,15 @@ struct GtBars {
     uint32_t tmem;
 };
 
-__device__ __forceinline__ uint32_t pack16(float a, float b, int fp16) {
-    if (fp16) {
+template <bool FP16>
+__device__ __forceinline__ uint32_t pack16(float a, float b) {
+    if constexpr (FP16) {
         __half2 h = __floats2half2_rn(a, b);
         return *reinterpret_cast<uint32_t *>(&h);
+    } else {
+        __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<uint32_t *>(&h);
     }
-    __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<uint32_t *>(&h);
 }
 __device__ __forceinline__ float2 unpack16(uint32_t v, int fp16) {
     if (fp16) return __half22float2(*reinterpret_cast<__half2 *>(&v));
@@ -123,14 +125,19 @@ __device__ __forceinline__ float2 unpack16(uint32_t v, int fp16) {
 
 // 32 values of this lane's row into a store tile of 32 rows: of 64 bytes (64-byte swizzle: 16-byte part c of row r at part
 // c ^ (r / 2 % 4)), or half h of 128 bytes (128-byte swizzle: part c at c ^ (r % 8)).
-__device__ __forceinline__ void stage16(uint8_t *buf, int lane, const float (&v)[32], int fp16, bool wide = false, int h = 0) {
+template <bool FP16>
+__device__ __forceinline__ void stage16_as(uint8_t *buf, int lane, const float (&v)[32], bool wide, int h) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-        const uint4 w = make_uint4(pack16(v[8 * c], v[8 * c + 1], fp16), pack16(v[8 * c + 2], v[8 * c + 3], fp16),
-                                   pack16(v[8 * c + 4], v[8 * c + 5], fp16), pack16(v[8 * c + 6], v[8 * c + 7], fp16));
+        const uint4 w = make_uint4(pack16<FP16>(v[8 * c], v[8 * c + 1]), pack16<FP16>(v[8 * c + 2], v[8 * c + 3]),
+                                   pack16<FP16>(v[8 * c + 4], v[8 * c + 5]), pack16<FP16>(v[8 * c + 6], v[8 * c + 7]));
         const int at = wide ? lane * 128 + (((4 * h + c) ^ (lane & 7)) << 4) : lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4);
         *reinterpret_cast<uint4 *>(buf + at) = w;
     }
+}
+__device__ __forceinline__ void stage16(uint8_t *buf, int lane, const float (&v)[32], int fp16, bool wide = false, int h = 0) {
+    if (fp16) stage16_as<true>(buf, lane, v, wide, h);
+    else stage16_as<false>(buf, lane, v, wide, h);
 }
 // 32 fp32 values: the whole 128-byte row (128-byte swizzle).
 __device__ __forceinline__ void stage32(uint8_t *buf, int lane, const float (&v)[32]) {
@@ -423,7 +430,7 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
     // Store tiles: two in turn where a tile has one output, else all at once.
     int turn = 0;
     auto acquire = [&]() {
-        if (lane == 0) {
+        if (elect_one()) {
             if (p.one_out) tma_wait_read<1>();
             else tma_wait_read<0>();
         }
@@ -504,7 +511,7 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
         }
         fence_async_smem();
         __syncwarp();
-        if (lane == 0 && in) {
+        if (in && elect_one()) {
             if (EPI == EPI_STORE && pr.add) tma_add(out, n, m0, buf);
             else tma_store(out, n, m0, buf);
             if (EPI == EPI_GATE_BWD || (EPI == EPI_GATE && !S8 && p.extra)) tma_store(out + 1, n, m0, buf + 2048);
@@ -514,7 +521,7 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
         if (p.one_out && in) turn ^= 1;
     };
 
-    const int sub_units = (EPI == EPI_GATE ? half : W) / unit_cols;
+    const int sub_cols = EPI == EPI_GATE ? half : W;   // output columns of a sub-tile
     if (p.splits == 1) {
         if (warp >= GT_EPI_W0) {
             const uint32_t empty0 = CG == 2 ? map_rank(&bar->acc_empty[0], even) : su32(&bar->acc_empty[0]);
@@ -529,12 +536,13 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
                 if (!mbar_wait(&bar->acc_full[slot], use & 1)) break;
                 tc_fence_after();
                 const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + GT_W * slot;
+                for (int sub = 0; sub < p.subs; ++sub)
 #pragma unroll 1
-                for (int u = team; u < sub_units * p.subs; u += 2)
-                    unit(pr, &maps.out[g], acc, u / sub_units, unit_cols * (u % sub_units), m0, n0, rs);
+                    for (int c = unit_cols * team; c < sub_cols; c += 2 * unit_cols)
+                        unit(pr, &maps.out[g], acc, sub, c, m0, n0, rs);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(empty0 + 8 * slot);   // the accumulators may be overwritten
+                if (elect_one()) mbar_arrive_cluster(empty0 + 8 * slot);   // the accumulators may be overwritten
             }
         }
     } else {
@@ -560,11 +568,13 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
         if (warp >= GT_EPI_W0) {
             float rs = 1.f;
             if constexpr (S8) rs = m0 + lane < pr.M ? p.row_scale[m0 + lane] : 0.f;
-            for (int u = split + p.splits * team; u < sub_units * p.subs; u += 2 * p.splits)
-                unit(pr, &maps.out[g], 0, u / sub_units, unit_cols * (u % sub_units), m0, n0, rs);
+            for (int sub = 0; sub < p.subs; ++sub)
+#pragma unroll 1
+                for (int c = unit_cols * (split + p.splits * team); c < sub_cols; c += 2 * unit_cols * p.splits)
+                    unit(pr, &maps.out[g], 0, sub, c, m0, n0, rs);
         }
     }
-    if (warp >= GT_EPI_W0 && lane == 0) tma_wait_read<0>();   // the stores have read shared memory; the grid's end completes them
+    if (warp >= GT_EPI_W0 && elect_one()) tma_wait_read<0>();   // the stores have read shared memory; the grid's end completes them
     __syncwarp();
     tc_fence_before();
     __syncthreads();
