@@ -691,14 +691,14 @@ int k_steps(const GemmArgs &g) {
     return (g.K + bk - 1) / bk * g.segs;
 }
 
-// The tile shape with the least modelled time, in SM cycles.  A k step takes the longest of its MMAs (2 cycles a column:
-// 128 rows x 64 values x 1 column at 4096 multiply-adds a cycle), its loads (72 bytes a cycle from L2 to an SM) and its
-// shared-memory traffic (the copies' writes and the MMAs' reads, 0.9 cycles a 128-byte row).  Narrow sub-tiles are
-// counted 4 % slower in long launches, where their extra traffic costs clock (4096 x 4096 x 8192 over and over: W = 192
-// 231 us, 256 222 us; one at a time 197 and 195).  A tile's epilogue takes 2700 cycles and 14.5 a column (the gate's
-// gradient, with its loads, 3.7 times that), hidden behind the next tile where there is one; a split adds the exchange,
-// 2000 cycles, 24.5 a column and 356 a CTA of the cluster; a pair 1250 to start.  Fitted to 2,700 timings of 85 products
-// (40 to 2,200 rows) on B200: the chosen shape is on average 1.7 % and at most 17 % slower than the fastest one.
+// The tile shape with the least modelled time, in SM cycles.  A k step takes the longer of its MMAs (2 cycles a column:
+// 128 rows x 64 values x 1 column at 4096 multiply-adds a cycle) and its shared-memory traffic (the copies' writes and
+// the MMAs' reads, 0.9 cycles a 128-byte row).  Narrow sub-tiles are counted 4 % slower in long launches, where their
+// extra traffic costs clock (4096 x 4096 x 8192 over and over: W = 192 231 us, 256 222 us; one at a time 197 and 195).  A
+// tile's epilogue takes 2820 cycles and 14 a column (the gate's gradient, with its loads, 56), hidden behind the next
+// tile where there is one; a split adds the exchange, 2400 cycles, 32 a column and 266 a CTA of the cluster; a pair 1770
+// to start.  Fitted to 6,700 timings of 118 products (24 to 2,200 rows) on B200: the chosen shape is on average 1.4 % and
+// at most 15 % slower than the fastest one.
 int choose(const GemmArgs &g, Shape *best, long long *time) {
     const int ksteps = k_steps(g);
     long long least = -1;
@@ -717,11 +717,11 @@ int choose(const GemmArgs &g, Shape *best, long long *time) {
                     const int tiles_n = (g.N + out - 1) / out, waves = (int)(((long long)tiles_m * tiles_n + room - 1) / room);
                     if (splits > 1 && C * 512 > GT_RING) break;    // the partial tile has to fit
                     const int br = b_rows(g.b_mn, W, cg);
-                    int step = std::max(2 * C, std::max((a_rows + subs * br) * GT_KB / 72, 9 * (a_rows * (subs + 1) + 2 * subs * br) / 10));
+                    int step = std::max(2 * C, 9 * (a_rows * (subs + 1) + 2 * subs * br) / 10);
                     if (W < GT_W && waves >= 3) step += step / 25;
-                    const long long main = (long long)kper * step, epi = 2700 + C * (g.epi == EPI_GATE_BWD ? 54 : 29 / 2);
-                    long long t = cg == 2 ? 1250 : 0;
-                    if (splits > 1) t += waves * (main + 2000 + 49 * C / 2 + 356 * cg * splits + epi / splits);
+                    const long long main = (long long)kper * step, epi = 2820 + C * (g.epi == EPI_GATE_BWD ? 56 : g.epi == EPI_GATE ? 15 : 14);
+                    long long t = cg == 2 ? 1770 : 0;
+                    if (splits > 1) t += waves * (main + 2400 + 32 * C + 266 * cg * splits + epi / splits);
                     else if (subs == 2) t += waves * (main + epi);
                     else t += (waves - 1) * std::max(main, epi) + main + epi;
                     if (least < 0 || t < least) {
@@ -737,28 +737,28 @@ int choose(const GemmArgs &g, Shape *best, long long *time) {
     return MOE_OK;
 }
 
-constexpr long long kLaunchCycles = 10300;   // a launch's own, in the models
+constexpr long long kLaunchCycles = 7600;   // a launch's own, in the models
 
 // The same for products in one launch (16-bit, B's row index contiguous, stored plainly; pairs, one sub-tile), and the
 // order of its tiles.  `big`: the first one's reduction is longer and its tiles go first.  Back to back, a k step takes
-// 1.18 times the above (shared memory serves the MMAs' reads and the copies' writes) and a tile 1600 cycles more.
+// 1.18 times the above and a tile 500 cycles more, or its share of HBM's write rate (1800 cycles and 5 a column).
 int choose_group(const GemmArgs *g, int n, bool big, Shape *best, int *rounds, long long *time) {
     long long least = -1;
     int room = 0;
     QE_TRY(active_clusters(2, &room));
     for (int W = 64; W <= GT_W; W += 64) {
-        const long long step = std::max(2 * W, (128 + b_rows(true, W, 2)) * GT_KB / 72), epi = 1800 + W * 29 / 2;
+        const long long step = std::max(2 * W, 18 * (128 + b_rows(true, W, 2)) / 10), epi = 1800 + 5 * W;
         long long t_big = 0, t_small = 0, n_big = 0, n_small = 0;
         for (int i = 0; i < n; ++i) {
             const long long tiles = (long long)((g[i].M + 255) / 256) * ((g[i].N + W - 1) / W);
-            const long long t = std::max(k_steps(g[i]) * step * 118 / 100 + 1600, epi);
+            const long long t = std::max(k_steps(g[i]) * step * 118 / 100 + 500, epi);
             if (big && i == 0) t_big = t, n_big = tiles;
             else t_small = t, n_small += tiles;
         }
         const long long over = n_big % room, rest = room - over;   // clusters with and without one more big tile
         for (long long r = 0; r <= (over ? n_small / rest : 0); ++r) {
             const long long after = (n_small - r * rest + room - 1) / room;
-            const long long t = 1250 + epi + n_big / room * t_big + std::max((over ? t_big : 0) + after * t_small, (r + after) * t_small);
+            const long long t = 1770 + epi + n_big / room * t_big + std::max((over ? t_big : 0) + after * t_small, (r + after) * t_small);
             if (least < 0 || t < least) {
                 least = t;
                 *best = {2, W, 1, 1};
@@ -892,10 +892,10 @@ int launch_gradients(const GemmArgs *dx, const GemmArgs *dw, int n_dw, cudaStrea
         for (int i = 0; i < n_dw; ++i) all[1 + i] = dw[i];
         QE_TRY(choose_group(all, 1 + n_dw, true, &sh, &rounds, &t_all));
         QE_TRY(choose(*dx, &sh_x, &t_x));
-        // one launch where that is modelled at least 5 % faster: its clusters with a tile of dx less take more of the
-        // others.  Measured on B200: 1001 rows of 2560 x 5120 80 us (two launches 107), 300 rows 58 (68), 4096 rows of
-        // 2048 x 4096 180 (203); but 600 rows of 1024 x 4096 36 (34), where dx alone splits its reduction.
-        if (100 * (t_all + kLaunchCycles) <= 95 * (t_x + t_w + 2 * kLaunchCycles))
+        // one launch where that is modelled faster: its clusters with a tile of dx less take more of the others.  Measured
+        // on B200: 1001 rows of 2560 x 5120 80 us (two launches 107), 300 rows 55 (62), 4096 rows of 2048 x 4096 180 (203);
+        // but 600 rows of 1024 x 4096 36 (34), where dx alone splits its reduction, 64 rows of 4096 x 8192 100 (74)
+        if (100 * (t_all + kLaunchCycles) <= 98 * (t_x + t_w + 2 * kLaunchCycles))
             return launch_group(all, 1 + n_dw, true, sh, rounds, st);
         QE_TRY(launch_shape(*dx, sh_x, st));
     }
