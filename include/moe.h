@@ -315,7 +315,7 @@ MOE_API int moe_route_static(const uint16_t *x_bf16, int T, int d_model, const f
  * (fp32, exact int32 for 8-bit operands) and results do not depend on timing:
  * the same call gives the same bits.  Errors: INVALID_ARG (also a workspace
  * that is too small: moe_last_error() names it), UNSUPPORTED (sizes outside
- * the limits), CUDA. */
+ * the limits, more than 2^30 rows), CUDA. */
 typedef enum { MOE_BF16 = 1, MOE_FP16 = 2, MOE_FP32 = 3 } moe_dtype;
 typedef enum {
     MOE_ACT_SILU = 1,       /* z / (1 + e^-z) */

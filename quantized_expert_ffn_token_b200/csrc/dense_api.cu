@@ -9,6 +9,7 @@ using namespace qeffn;
 
 namespace {
 
+constexpr int kMaxRows = 1 << 30;
 constexpr int kMaxDim = 65536;   // 127 * 127 * 65536 < 2^31: an 8-bit product's sum stays in int32
 
 int bad(const char *what) { return set_error(MOE_ERR_INVALID_ARG, what); }
@@ -61,6 +62,11 @@ int check_workspace(const void *ws, long long have, long long need) {
     if (!ws || have < need) return bad("workspace: smaller than the *_workspace call names");
     if (!aligned(ws, 256)) return bad("workspace: not 256-byte aligned");
     return MOE_OK;
+}
+
+int check_rows(int T) {
+    if (T < 0) return bad("T is negative");
+    return T <= kMaxRows ? MOE_OK : unsupported("T: at most 2^30");
 }
 
 int check_act(int act) {
@@ -138,7 +144,7 @@ int moe_ffn_workspace(const moe_ffn *f, int T, int backward, long long *bytes) {
 int moe_ffn_forward(const moe_ffn *f, const void *x, long long ld_x, int T, void *y, long long ld_y, void *gate,
                     void *up, void *workspace, long long workspace_bytes, void *stream) {
     QE_TRY(check_ffn(f));
-    if (T < 0) return bad("T is negative");
+    QE_TRY(check_rows(T));
     if (T == 0) return MOE_OK;
     if (!x || !y || !f->w_gate || !f->w_up || !f->w_down) return bad("NULL x, y or weights");
     if ((gate == nullptr) != (up == nullptr)) return bad("gate and up: both or neither");
@@ -175,7 +181,7 @@ int moe_ffn_backward(const moe_ffn *f, const void *x, long long ld_x, const void
                      long long ld_dy, int T, void *dx, long long ld_dx, void *dw_gate, void *dw_up, void *dw_down,
                      int flags, void *workspace, long long workspace_bytes, void *stream) {
     QE_TRY(check_ffn(f));
-    if (T < 0) return bad("T is negative");
+    QE_TRY(check_rows(T));
     if (flags & ~(MOE_FFN_GRAD_FP32 | MOE_FFN_GRAD_ADD)) return bad("flags: unknown bits");
     if ((flags & MOE_FFN_GRAD_ADD) && !(flags & MOE_FFN_GRAD_FP32)) return bad("MOE_FFN_GRAD_ADD needs MOE_FFN_GRAD_FP32");
     const bool dw = dw_gate || dw_up || dw_down;
@@ -244,7 +250,8 @@ int moe_ffn_backward(const moe_ffn *f, const void *x, long long ld_x, const void
 int moe_quantize_s8(const void *x, int dtype, long long ld_x, int rows, int cols, int8_t *q, float *scale,
                     void *stream) {
     if (dtype != MOE_BF16 && dtype != MOE_FP16 && dtype != MOE_FP32) return bad("dtype: not a moe_dtype");
-    if (rows < 0 || cols <= 0) return bad("rows must not be negative, cols must be positive");
+    QE_TRY(check_rows(rows));
+    if (cols <= 0) return bad("cols must be positive");
     if (cols > kMaxDim) return unsupported("cols: at most 65536");
     if (rows == 0) return MOE_OK;
     if (!x || !q || !scale) return bad("NULL x, q or scale");
@@ -266,7 +273,8 @@ int moe_matmul_s8(const int8_t *a, const float *a_scale, int T, const int8_t *w,
                   const float *bias, void *y, int y_dtype, long long ld_y, void *workspace, long long workspace_bytes,
                   void *stream) {
     if (y_dtype != MOE_BF16 && y_dtype != MOE_FP16 && y_dtype != MOE_FP32) return bad("y_dtype: not a moe_dtype");
-    if (T < 0 || N <= 0 || K <= 0) return bad("T must not be negative, N and K must be positive");
+    QE_TRY(check_rows(T));
+    if (N <= 0 || K <= 0) return bad("N and K must be positive");
     if (K % 16 != 0 || K > kMaxDim || N % 8 != 0) return unsupported("K: a multiple of 16 up to 65536; N: a multiple of 8");
     if (T == 0) return MOE_OK;
     if (!a || !a_scale || !w || !w_scale || !y) return bad("NULL a, w, scales or y");
@@ -298,7 +306,7 @@ int moe_ffn_s8_workspace(const moe_ffn_s8 *f, int T, long long *bytes) {
 int moe_ffn_s8_forward(const moe_ffn_s8 *f, const void *x, long long ld_x, int T, void *y, long long ld_y,
                        void *workspace, long long workspace_bytes, void *stream) {
     QE_TRY(check_ffn_s8(f));
-    if (T < 0) return bad("T is negative");
+    QE_TRY(check_rows(T));
     if (T == 0) return MOE_OK;
     if (!x || !y || !f->w_gate || !f->w_up || !f->w_down || !f->s_gate || !f->s_up || !f->s_down)
         return bad("NULL x, y, weights or scales");

@@ -14,13 +14,16 @@ __expf(x) within 2 + 1.17 |x| units in the last place, |x| < 89 where it is not
 zero, i.e. 107 * 2^-23 < 2^-16.
 """
 import ctypes
+import os
+import subprocess
+import sys
 
-import numpy as np
 import pytest
 import torch
 
 from quantized_expert_ffn_token_b200 import capi
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 U = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24}
 U32 = 2.0 ** -19
 UACT = 2.0 ** -16
@@ -89,6 +92,7 @@ def test_ffn_refusals():
     assert fwd(_ffn(I=516)) == uns
     assert fwd(_ffn(d=65544)) == uns
     assert fwd(_ffn(), T=-1) == inv
+    assert fwd(_ffn(), T=(1 << 30) + 1) == uns
     assert fwd(_ffn(), x=None) == inv
     assert fwd(_ffn(w=None)) == inv
     assert fwd(_ffn(), g=P) == inv
@@ -575,6 +579,62 @@ def test_captured_calls_replay(T):
         check_backward(x, g, u, dy, wg, wu, wd, "silu", out)
         check_ffn_s8(x, wq, "silu", y8)
     assert capi.moe_ffn_get_device_error() == 0
+
+
+@pytest.mark.gpu
+def test_capture_in_a_fresh_process():
+    """A process whose first calls of the operators are captured ones."""
+    code = """
+import sys, torch
+sys.path.insert(0, {root!r})
+from tests.test_dense_ffn import *
+from tests.test_dense_ffn import _mk, _ws, _quantized
+T, d, I, dt = 150, 256, 512, torch.bfloat16
+x, wg, wu, wd, dy, rnd = _mk(1, T, d, I, dt)
+f = capi.make_ffn(wg, wu, wd)
+y, g, u = torch.empty_like(x), x.new_empty(T, I), x.new_empty(T, I)
+out = [torch.empty_like(v) for v in (x, wg, wu, wd)]
+ws, wb = _ws(capi.moe_ffn_workspace(f, T)), _ws(capi.moe_ffn_workspace(f, T, True))
+q, s, x1, y1 = torch.empty(T, d, dtype=torch.int8, device="cuda"), torch.empty(T, device="cuda"), x[:3].clone(), y[:3].clone()
+st = torch.cuda.Stream()
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph, stream=st):
+    capi.moe_ffn_forward(f, x, T, y, g, u, ws, st)
+    capi.moe_ffn_backward(f, x, g, u, dy, T, *out, workspace=wb, stream=st)
+    capi.moe_quantize_s8(x, q, s, st)
+    capi.moe_ffn_forward(f, x1, 3, y1, workspace=ws, stream=st)
+graph.replay()
+torch.cuda.synchronize()
+check_forward(x, wg, wu, wd, "silu", y, g, u)
+check_backward(x, g, u, dy, wg, wu, wd, "silu", out)
+check_forward(x1, wg, wu, wd, "silu", y1, None, None)
+assert torch.equal(q.double(), quantize64(x)[0])
+print("captured")
+""".format(root=ROOT)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, cwd=ROOT)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits():
+    """Intermediates of more than 2^31 elements: the last rows are as they are in a call of their own."""
+    T, d, I, dt = 33100, 64, 65536, torch.bfloat16
+    x, wg, wu, wd, dy, _ = _mk(5, T, d, I, dt)
+    f = capi.make_ffn(wg, wu, wd)
+    y, g, u = _forward(f, x)
+    n = 40
+    check_forward(x[-n:], wg, wu, wd, "silu", y[-n:], g[-n:], u[-n:])
+    dx = torch.full_like(x, float("nan"))
+    ws = _ws(capi.moe_ffn_workspace(f, T, True))
+    capi.moe_ffn_backward(f, x, g, u, dy, T, dx, workspace=ws)
+    check_backward(x[-n:], g[-n:], u[-n:], dy[-n:], wg, wu, wd, "silu", [dx[-n:], None, None, None])
+    del y, u, dx, ws
+    wq = [_quantized(w) for w in (wg, wu, wd)]
+    f8 = capi.make_ffn_s8(*wq[0], *wq[1], *wq[2], "silu", dt)
+    y8 = torch.full_like(x, float("nan"))
+    capi.moe_ffn_s8_forward(f8, x, T, y8, _ws(capi.moe_ffn_s8_workspace(f8, T)))
+    check_ffn_s8(x[-n:], wq, "silu", y8[-n:])
 
 
 @pytest.mark.gpu
