@@ -533,6 +533,14 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
                 float rs = 1.f;
                 if constexpr (S8) rs = m0 + lane < pr.M ? p.row_scale[m0 + lane] : 0.f;
                 const int slot = two_acc ? n & 1 : 0, use = two_acc ? n >> 1 : n;
+                if constexpr (EPI == EPI_GATE_BWD)   // gate and up of this row: on their way to L2 while the MMAs run
+                    if (m0 + lane < pr.M) {
+                        const long long at = (long long)(m0 + lane) * pr.N;
+                        for (int c = n0 + 64 * team; c < min(n0 + tile_cols, pr.N); c += 128) {
+                            prefetch_l2((const uint16_t *)p.in1 + at + c);
+                            prefetch_l2((const uint16_t *)p.in2 + at + c);
+                        }
+                    }
                 if (!mbar_wait(&bar->acc_full[slot], use & 1)) break;
                 tc_fence_after();
                 const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + GT_W * slot;
@@ -746,7 +754,7 @@ int choose_group(const GemmArgs *g, int n, bool big, Shape *best, int *rounds, l
     long long least = -1;
     int room = 0;
     QE_TRY(active_clusters(2, &room));
-    for (int W = 64; W <= GT_W; W += 64) {
+    for (int W = big ? 192 : 128; W <= GT_W; W += 64) {   // narrower tiles never measured faster
         const long long step = std::max(2 * W, 18 * (128 + b_rows(true, W, 2)) / 10), epi = 1800 + 5 * W;
         long long t_big = 0, t_small = 0, n_big = 0, n_small = 0;
         for (int i = 0; i < n; ++i) {
@@ -892,10 +900,11 @@ int launch_gradients(const GemmArgs *dx, const GemmArgs *dw, int n_dw, cudaStrea
         for (int i = 0; i < n_dw; ++i) all[1 + i] = dw[i];
         QE_TRY(choose_group(all, 1 + n_dw, true, &sh, &rounds, &t_all));
         QE_TRY(choose(*dx, &sh_x, &t_x));
-        // one launch where that is modelled faster: its clusters with a tile of dx less take more of the others.  Measured
-        // on B200: 1001 rows of 2560 x 5120 80 us (two launches 107), 300 rows 55 (62), 4096 rows of 2048 x 4096 180 (203);
-        // but 600 rows of 1024 x 4096 36 (34), where dx alone splits its reduction, 64 rows of 4096 x 8192 100 (74)
-        if (100 * (t_all + kLaunchCycles) <= 98 * (t_x + t_w + 2 * kLaunchCycles))
+        // one launch where that is modelled at least 7 % faster: its clusters with a tile of dx less take more of the
+        // others.  Measured on B200: 1001 rows of 2560 x 5120 102 us (two launches 113), 500 rows of 4000 x 2000 38 (47),
+        // 1500 rows of 1024 x 1024 21.6 (24.5); but 600 rows of 1024 x 4096 47 (48), 150 rows of 2048 x 8192 84 (60),
+        // where dx alone splits its reduction
+        if (100 * (t_all + kLaunchCycles) <= 93 * (t_x + t_w + 2 * kLaunchCycles))
             return launch_group(all, 1 + n_dw, true, sh, rounds, st);
         QE_TRY(launch_shape(*dx, sh_x, st));
     }
