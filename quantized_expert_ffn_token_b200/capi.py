@@ -288,17 +288,17 @@ def _rows(t, T: int, cols: int, dtype, what: str):
 
 def _full(t, shape, dtype, what: str):
     """Address of a contiguous CUDA tensor of this shape and torch dtype."""
-    if t.shape != shape or t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{what}: a contiguous CUDA tensor {list(shape)} of {dtype} expected")
-    return t.data_ptr()
+    if t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{what}: a contiguous CUDA tensor {list(shape)} of {dtype} expected")
 
 
 def _space(ws):
     if ws is None:
         return None, 0
-    if not ws.is_cuda or not ws.is_contiguous():
-        raise ValueError("workspace: a contiguous CUDA tensor expected")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
+    if ws.is_cuda and ws.is_contiguous():
+        return ws.data_ptr(), ws.numel() * ws.element_size()
+    raise ValueError("workspace: a contiguous CUDA tensor expected")
 
 
 def _act(act) -> int:
@@ -358,14 +358,10 @@ def moe_ffn_backward(f: moe_ffn, x, gate, up, dy, T: int, dx=None, dw_gate=None,
 
 
 def _codes(t, shape, what: str):
-    if t.dtype is not torch.int8:
-        raise ValueError(f"{what}: int8 expected")
     return _full(t, shape, torch.int8, what)
 
 
 def _scales(t, n: int, what: str):
-    if t.dtype is not torch.float32:
-        raise ValueError(f"{what}: fp32 expected")
     return _full(t, (n,), torch.float32, what)
 
 

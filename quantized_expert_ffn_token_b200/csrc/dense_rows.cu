@@ -180,21 +180,31 @@ int launch_rows_as(const RowsArgs &p, cudaStream_t st) {
     return MOE_OK;
 }
 
-// Shapes, measured on B200 (launches back to back, each waiting for the last; bf16 unless said):
-//   one token, gate and up 2 x 10240 x 2560: 8 warps, 2 CTAs per SM 6000 GB/s (3: 5620, 4 warps x 6: 5270, 16 x 2: 5130)
-//   one token, 2560 x 10240: 8 warps with 4 blocks in flight 4410 GB/s (2 blocks: 4000, 4 warps: 3180, 16 warps: 3840)
-//   a grid below the SM count: 16 warps (2 x 512 x 2560, one token: 1600 GB/s, 8 warps 1410; 1024 x 6000, 12 tokens: 6.2
-//   us, 8 warps 7.7; two row groups a CTA 7.6)
-//   several tokens, more rows than that: two row groups a CTA, because the token operand costs as much as the weights;
-//   16 warps for up to 4096 rows or rows of 64 blocks (2048 x 1024, 32 tokens: 2.9 us, one group 3.8; 2560 x 10240, 16
-//   tokens: 16.9, 8 warps 20.9), else 4 warps (10240 x 2560 8-bit, 16 tokens: 8.0, one group 9.5, 16 warps 10.8)
+// Shapes, measured on B200 in us (launches back to back, each waiting for the last; rows x bytes a row).  A block is 128
+// bytes of a row; `brief` rows have fewer than 32.
+//   gate and up, one token: 8 warps, 2 CTAs an SM 10240 x 5120 17.5 (3 CTAs 18.6, 4 warps x 6 19.9, 16 x 2 20.5); many brief
+//   rows 4 warps with 2 blocks in flight 5000 x 1024 3.6 (8 warps 4.5), 6000 x 2048 6.3 (6.5), at 16 tokens 4
+//   warps x 6 CTAs 7.0 (8.0); but 2048 x 2048 8 warps, 3.5 (3.6 and more)
+//   a grid below the SM count: 16 warps (2 x 512 x 5120 3.3, 8 warps 3.7; 1024 x 12000, 12 tokens 6.2, 8 warps 7.7)
+//   one matrix, one token: 2560 x 20480 8 warps with 4 blocks in flight 11.8 (2 blocks 13.1, 4 warps 16.5, 16 warps 13.7);
+//   two row groups a CTA for more rows, 16 warps 12288 x 8192 18.7 (20.3), and for brief rows, 4 warps 10240 x 2560 6.0 (7.3)
+//   one matrix, several tokens: two row groups a CTA, because the token operand costs as much as the weights; 16 warps for
+//   up to 4096 rows or rows of 64 blocks (2048 x 2048, 32 tokens 2.9, one group 3.8; 2560 x 20480, 16 tokens 16.9, 8 warps
+//   20.9), else 4 warps (10240 x 2560 8-bit, 16 tokens 8.0, one group 9.5, 16 warps 10.8)
 template <int TYPE, int TT>
 int launch_rows_t(const RowsArgs &p, bool gate, cudaStream_t st) {
-    const bool few = p.N <= 8 * 148;
-    if (gate)
-        return few ? launch_rows_as<TYPE, TT, true, 1, 16, 1, 1>(p, st) : launch_rows_as<TYPE, TT, true, 1, 8, 1, 2>(p, st);
+    const bool few = p.N <= 8 * 148, brief = p.Kb < 32 * 128;
+    if (gate) {
+        if (few) return launch_rows_as<TYPE, TT, true, 1, 16, 1, 1>(p, st);
+        if (!brief || p.N <= 4096) return launch_rows_as<TYPE, TT, true, 1, 8, 1, 2>(p, st);
+        if constexpr (TT == 1) return launch_rows_as<TYPE, TT, true, 1, 4, 2, 4>(p, st);
+        return launch_rows_as<TYPE, TT, true, 1, 4, 1, 6>(p, st);
+    }
     if (few) return launch_rows_as<TYPE, TT, false, 1, 16, 2, 1>(p, st);
-    if constexpr (TT == 1) return launch_rows_as<TYPE, TT, false, 1, 8, 4, 3>(p, st);
+    if constexpr (TT == 1) {
+        if (brief) return launch_rows_as<TYPE, TT, false, 2, 4, 2, 4>(p, st);
+        return p.N > 4096 ? launch_rows_as<TYPE, TT, false, 2, 16, 1, 2>(p, st) : launch_rows_as<TYPE, TT, false, 1, 8, 4, 3>(p, st);
+    }
     if (p.N <= 4096 || p.Kb >= 64 * 128) return launch_rows_as<TYPE, TT, false, 2, 16, 1, 2>(p, st);
     return launch_rows_as<TYPE, TT, false, 2, 4, 1, 6>(p, st);
 }
