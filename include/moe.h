@@ -401,7 +401,8 @@ MOE_API int moe_ffn_s8_forward(const moe_ffn_s8 *f, const void *x, long long ld_
 
 /* Read (and clear) the error word of the calls above on the current device
  * (their kernels' bounded waits set it; *code receives 0 or a MOE_ERR_*
- * value).  Synchronises the device. */
+ * value).  After a nonzero code the results since the last call of this are
+ * undefined.  Synchronises the device. */
 MOE_API int moe_ffn_get_device_error(int *code);
 
 /* Static text for a status code. */

@@ -335,13 +335,16 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
                 if (++s == p.stages) s = 0, phase ^= 1;
             }
         }
-        // every copy has landed before the CTAs leave: the last fills that no MMA waited for
-        if (!ok && rank == 0)
+        // after a failed wait every copy has to land before the CTAs leave: the last fills, which no MMA waited for, and
+        // B requested ahead for fills that never came (their barriers stay open: the wait runs its full time)
+        if (!ok && rank == 0) {
+            for (int j = filled; j < early; ++j) mbar_wait(&bar->full[j], 0, true);
             for (int j = 0; j < p.stages && j < filled; ++j) {
                 if (s == 0) s = p.stages, phase ^= 1;
                 --s;
                 mbar_wait(&bar->full[s], phase, true);
             }
+        }
         __syncwarp();
     } else if (warp == 1 && rank == 0) {
         const uint32_t idesc = (S8 ? (2u << 4) | (1u << 7) | (1u << 10)
@@ -621,7 +624,8 @@ int encode(CUtensorMap *m, int dtype, const void *p, long long inner, long long 
     const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer}, strides[1] = {(cuuint64_t)ld * size};
     const cuuint32_t box[2] = {(cuuint32_t)box_inner, (cuuint32_t)box_outer}, es[2] = {1, 1};
     const CUresult r = fn(m, t, 2, const_cast<void *>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          box_inner * size == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                          box_inner * size == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? MOE_OK : set_error(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed");
 }
 
