@@ -118,9 +118,23 @@ __device__ __forceinline__ uint32_t pack16(float a, float b) {
         return *reinterpret_cast<uint32_t *>(&h);
     }
 }
-__device__ __forceinline__ float2 unpack16(uint32_t v, int fp16) {
-    if (fp16) return __half22float2(*reinterpret_cast<__half2 *>(&v));
-    return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162 *>(&v));
+// 32 values of four 16-byte loads (the type's branch outside the loop, as with the activations below).
+template <bool FP16>
+__device__ __forceinline__ void unpack_as(const uint4 (&w)[4], float (&v)[32]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t e[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = FP16 ? __half22float2(*reinterpret_cast<const __half2 *>(&e[i]))
+                                  : make_float2(__uint_as_float(e[i] << 16), __uint_as_float(e[i] & 0xFFFF0000u));
+            v[8 * j + 2 * i] = f.x, v[8 * j + 2 * i + 1] = f.y;
+        }
+    }
+}
+__device__ __forceinline__ void unpack16(const uint4 (&w)[4], float (&v)[32], int fp16) {
+    if (fp16) unpack_as<true>(w, v);
+    else unpack_as<false>(w, v);
 }
 
 // 32 values of this lane's row into a store tile of 32 rows: of 64 bytes (64-byte swizzle: 16-byte part c of row r at part
@@ -497,16 +511,8 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
             get(acc, col, v);
             buf = acquire();
             float du[32], hh[32];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t gs[4] = {gw[j].x, gw[j].y, gw[j].z, gw[j].w}, us[4] = {uw[j].x, uw[j].y, uw[j].z, uw[j].w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 z = unpack16(gs[i], p.fp16), u = unpack16(us[i], p.fp16);
-                    const int e = 8 * j + 2 * i;
-                    hh[e] = z.x, hh[e + 1] = z.y, du[e] = u.x, du[e + 1] = u.y;
-                }
-            }
+            unpack16(gw, hh, p.fp16);
+            unpack16(uw, du, p.fp16);
             gate_bwd_all(p.act, v, du, hh);
             stage16(buf, lane, v, p.fp16);
             stage16(buf + 2048, lane, du, p.fp16);
