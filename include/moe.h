@@ -361,9 +361,11 @@ MOE_API int moe_ffn_backward(const moe_ffn *f, const void *x, long long ld_x, co
 
 /* Rows of x [rows][cols] (bf16, fp16 or fp32) as 8-bit codes and one scale a
  * row:  scale = max|x| / 127 (fp32),  q = x / scale, rounded to fp32, then to
- * the nearest whole number (half to even).  A row of zeros (or one whose scale
- * underflows to zero) has scale 0 and codes 0; a row with a NaN or an infinity
- * has scale NaN and codes 0, so that every product of it is NaN.  q
+ * the nearest whole number (half to even), and held within +-127 (a quotient
+ * exceeds that only where the scale is subnormal and its rounding coarse: fp32
+ * rows whose largest magnitude is below 2.3e-41).  A row of zeros (or one
+ * whose scale underflows to zero) has scale 0 and codes 0; a row with a NaN or
+ * an infinity has scale NaN and codes 0, so that every product of it is NaN.  q
  * [rows][cols] is contiguous.  x may have any row distance of at least cols
  * and needs the alignment of its type only. */
 MOE_API int moe_quantize_s8(const void *x, int dtype, long long ld_x, int rows, int cols, int8_t *q, float *scale,

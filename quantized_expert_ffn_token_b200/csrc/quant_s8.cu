@@ -36,11 +36,14 @@ __device__ __forceinline__ RowScale row_scale(unsigned top) {
     return s > 1e-37f ? RowScale{s, __fdiv_rn(1.f, s), 0.4999f, finite} : RowScale{s, 0.f, -1.f, finite && s > 0.f};
 }
 
-// Four codes by division, for values next to a half (kept out of line: inlined, its copies did not fit the instruction
-// cache and the kernel took five times as long).
+// A code by division.  A subnormal scale is rounded to whole units of 2^-149, by up to a third of itself: quotients reach
+// 190 there (a maximum of 190 units has the scale 1), and their codes are held at 127.
+__device__ __forceinline__ int code_exact(float v, float s) { return max(-127, min(127, __float2int_rn(__fdiv_rn(v, s)))); }
+// Four of them, for values next to a half (kept out of line: inlined, its copies did not fit the instruction cache and the
+// kernel took five times as long).
 __device__ __noinline__ uint32_t codes_exact(float a, float b, float c, float d, float s) {
-    return (uint32_t)(__float2int_rn(__fdiv_rn(a, s)) & 255) | (uint32_t)(__float2int_rn(__fdiv_rn(b, s)) & 255) << 8 |
-           (uint32_t)(__float2int_rn(__fdiv_rn(c, s)) & 255) << 16 | (uint32_t)(__float2int_rn(__fdiv_rn(d, s)) & 255) << 24;
+    return (uint32_t)(code_exact(a, s) & 255) | (uint32_t)(code_exact(b, s) & 255) << 8 |
+           (uint32_t)(code_exact(c, s) & 255) << 16 | (uint32_t)(code_exact(d, s) & 255) << 24;
 }
 // Four codes.  Adding 1.5 * 2^23 rounds the product with the reciprocal to a whole number (half to even) in the sum's
 // low bits.
@@ -115,7 +118,7 @@ __global__ void __launch_bounds__(NT) k_quantize_s8(const T *x, long long ld, in
         for (int j = 0; j < NV; ++j)
             if (at + j * LANES < nvec) put_codes<T>(qr, at + j * LANES, held[j], r);
     } else {
-        for (int i = at; i < cols; i += LANES) qr[i] = r.live ? (int8_t)__float2int_rn(__fdiv_rn(to_f32(xr[i]), r.s)) : (int8_t)0;
+        for (int i = at; i < cols; i += LANES) qr[i] = r.live ? (int8_t)code_exact(to_f32(xr[i]), r.s) : (int8_t)0;
     }
 }
 
