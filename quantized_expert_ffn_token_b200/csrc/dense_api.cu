@@ -9,7 +9,7 @@ using namespace qeffn;
 
 namespace {
 
-constexpr int kMaxRows = 1 << 30;
+constexpr int kMaxRows = 1 << 30;   // of either operand: the kernels' row and column indices, a tile past the end, are 32-bit
 constexpr int kMaxDim = 65536;   // 127 * 127 * 65536 < 2^31: an 8-bit product's sum stays in int32
 
 int bad(const char *what) { return set_error(MOE_ERR_INVALID_ARG, what); }
@@ -275,7 +275,8 @@ int moe_matmul_s8(const int8_t *a, const float *a_scale, int T, const int8_t *w,
     if (y_dtype != MOE_BF16 && y_dtype != MOE_FP16 && y_dtype != MOE_FP32) return bad("y_dtype: not a moe_dtype");
     QE_TRY(check_rows(T));
     if (N <= 0 || K <= 0) return bad("N and K must be positive");
-    if (K % 16 != 0 || K > kMaxDim || N % 8 != 0) return unsupported("K: a multiple of 16 up to 65536; N: a multiple of 8");
+    if (K % 16 != 0 || K > kMaxDim || N % 8 != 0 || N > kMaxRows)
+        return unsupported("K: a multiple of 16 up to 65536; N: a multiple of 8 up to 2^30");
     if (T == 0) return MOE_OK;
     if (!a || !a_scale || !w || !w_scale || !y) return bad("NULL a, w, scales or y");
     if (!ptrs16({a, w, y}) || !aligned(a_scale, 4) || !aligned(w_scale, 4) || !aligned(bias, 4))

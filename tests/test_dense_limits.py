@@ -6,6 +6,19 @@ import torch
 from quantized_expert_ffn_token_b200 import capi
 
 
+# ---- sizes: refused before a device is touched -------------------------------------------------------------------
+
+P = 0x100000            # an aligned address that no device has: a call that gets as far as looking at it fails otherwise
+
+
+@pytest.mark.parametrize("N", [(1 << 30) + 8, (1 << 31) - 16, (1 << 31) - 8])
+@pytest.mark.parametrize("T", [1, 16, 200])
+def test_product_refuses_more_columns_than_its_indices_hold(T, N):
+    """Row and column indices of the kernels are 32-bit: the last block of 8 or 16 rows of w would start past 2^31."""
+    st = capi.lib.moe_matmul_s8(P, P, T, P, P, N, 16, None, P, capi.MOE_BF16, 0, None, 0, None)
+    assert st == capi.MOE_ERR_UNSUPPORTED and "N" in capi.last_error()
+
+
 # ---- rows whose scale is a small subnormal number ----------------------------------------------------------------
 
 UNIT = 2.0 ** -149      # fp32's smallest positive number
