@@ -262,6 +262,12 @@ def make_record(x=None, y=None, y_f32=None, ids=None, w=None, rows=None) -> moe_
 # Tensors carry their sizes here: activations are 2-d CUDA tensors whose rows may lie apart (a slice of a wider
 # buffer); everything else is contiguous.  Shapes and types are checked before an address leaves Python.
 
+def _int(n: int) -> int:
+    """n as a C int.  ctypes takes a size modulo 2^32; past its range it becomes the nearest C int, which is
+    outside every call's limits."""
+    return n if -0x80000000 <= n <= 0x7FFFFFFF else 0x7FFFFFFF if n > 0 else -0x80000000
+
+
 def _dtype(t) -> int:
     try:
         return DTYPES[t.dtype]
@@ -309,7 +315,7 @@ def make_ffn(w_gate, w_up, w_down, act="silu") -> moe_ffn:
     """The block over its weights [d_ff, d_model], [d_ff, d_model], [d_model, d_ff] (kept alive by the result)."""
     I, d = w_gate.shape
     f = moe_ffn()
-    f.d_model, f.d_ff, f.dtype, f.act = d, I, _dtype(w_gate), _act(act)
+    f.d_model, f.d_ff, f.dtype, f.act = _int(d), _int(I), _dtype(w_gate), _act(act)
     f.torch_dtype = w_gate.dtype
     f.w_gate = _full(w_gate, (I, d), f.torch_dtype, "w_gate")
     f.w_up = _full(w_up, (I, d), f.torch_dtype, "w_up")
@@ -321,7 +327,7 @@ def make_ffn(w_gate, w_up, w_down, act="silu") -> moe_ffn:
 
 def moe_ffn_workspace(f: moe_ffn, T: int, backward: bool = False) -> int:
     n = ctypes.c_longlong()
-    _check(lib.moe_ffn_workspace(f.ref, T, 1 if backward else 0, ctypes.byref(n)), "moe_ffn_workspace")
+    _check(lib.moe_ffn_workspace(f.ref, _int(T), 1 if backward else 0, ctypes.byref(n)), "moe_ffn_workspace")
     return n.value
 
 
@@ -332,7 +338,7 @@ def moe_ffn_forward(f: moe_ffn, x, T: int, y, gate=None, up=None, workspace=None
     gp = None if gate is None else _full(gate, (T, I), dt, "gate")
     up_ = None if up is None else _full(up, (T, I), dt, "up")
     wp, wn = _space(workspace)
-    _check(lib.moe_ffn_forward(f.ref, xp, lx, T, yp, ly, gp, up_, wp, wn, _stream(stream)),
+    _check(lib.moe_ffn_forward(f.ref, xp, lx, _int(T), yp, ly, gp, up_, wp, wn, _stream(stream)),
            "moe_ffn_forward")
 
 
@@ -353,7 +359,7 @@ def moe_ffn_backward(f: moe_ffn, x, gate, up, dy, T: int, dx=None, dw_gate=None,
     du = None if dw_up is None else _full(dw_up, (I, d), wdt, "dw_up")
     dd = None if dw_down is None else _full(dw_down, (d, I), wdt, "dw_down")
     wp, wn = _space(workspace)
-    _check(lib.moe_ffn_backward(f.ref, xp, lx, gp, up_, dyp, ldy, T, dxp, ldx, dg, du, dd, flags, wp, wn,
+    _check(lib.moe_ffn_backward(f.ref, xp, lx, gp, up_, dyp, ldy, _int(T), dxp, ldx, dg, du, dd, flags, wp, wn,
                                 _stream(stream)), "moe_ffn_backward")
 
 
@@ -369,13 +375,13 @@ def moe_quantize_s8(x, q, scale, stream=None) -> None:
     """Rows of x (bf16, fp16, fp32) as 8-bit codes q [rows, cols] and scales [rows]."""
     rows, cols = x.shape
     xp, lx = _rows(x, rows, cols, x.dtype, "x")
-    _check(lib.moe_quantize_s8(xp, _dtype(x), lx, rows, cols, _codes(q, (rows, cols), "q"),
+    _check(lib.moe_quantize_s8(xp, _dtype(x), lx, _int(rows), _int(cols), _codes(q, (rows, cols), "q"),
                                _scales(scale, rows, "scale"), _stream(stream)), "moe_quantize_s8")
 
 
 def moe_matmul_s8_workspace(T: int, N: int, K: int) -> int:
     n = ctypes.c_longlong()
-    _check(lib.moe_matmul_s8_workspace(T, N, K, ctypes.byref(n)), "moe_matmul_s8_workspace")
+    _check(lib.moe_matmul_s8_workspace(_int(T), _int(N), _int(K), ctypes.byref(n)), "moe_matmul_s8_workspace")
     return n.value
 
 
@@ -385,8 +391,9 @@ def moe_matmul_s8(a, a_scale, w, w_scale, y, bias=None, workspace=None, stream=N
     N = w.shape[0]
     yp, ly = _rows(y, T, N, y.dtype, "y")
     wp, wn = _space(workspace)
-    _check(lib.moe_matmul_s8(_codes(a, (T, K), "a"), _scales(a_scale, T, "a_scale"), T, _codes(w, (N, K), "w"),
-                             _scales(w_scale, N, "w_scale"), N, K, None if bias is None else _scales(bias, N, "bias"),
+    _check(lib.moe_matmul_s8(_codes(a, (T, K), "a"), _scales(a_scale, T, "a_scale"), _int(T), _codes(w, (N, K), "w"),
+                             _scales(w_scale, N, "w_scale"), _int(N), _int(K),
+                             None if bias is None else _scales(bias, N, "bias"),
                              yp, _dtype(y), ly, wp, wn, _stream(stream)), "moe_matmul_s8")
 
 
@@ -394,7 +401,7 @@ def make_ffn_s8(w_gate, s_gate, w_up, s_up, w_down, s_down, act="silu", dtype=No
     """The block over 8-bit weights and their row scales; ``dtype``: torch.bfloat16 or torch.float16 of x and y."""
     I, d = w_gate.shape
     f = moe_ffn_s8()
-    f.d_model, f.d_ff, f.dtype, f.act = d, I, DTYPES.get(dtype, 0), _act(act)
+    f.d_model, f.d_ff, f.dtype, f.act = _int(d), _int(I), DTYPES.get(dtype, 0), _act(act)
     f.torch_dtype = dtype
     f.w_gate, f.s_gate = _codes(w_gate, (I, d), "w_gate"), _scales(s_gate, I, "s_gate")
     f.w_up, f.s_up = _codes(w_up, (I, d), "w_up"), _scales(s_up, I, "s_up")
@@ -406,7 +413,7 @@ def make_ffn_s8(w_gate, s_gate, w_up, s_up, w_down, s_down, act="silu", dtype=No
 
 def moe_ffn_s8_workspace(f: moe_ffn_s8, T: int) -> int:
     n = ctypes.c_longlong()
-    _check(lib.moe_ffn_s8_workspace(f.ref, T, ctypes.byref(n)), "moe_ffn_s8_workspace")
+    _check(lib.moe_ffn_s8_workspace(f.ref, _int(T), ctypes.byref(n)), "moe_ffn_s8_workspace")
     return n.value
 
 
@@ -414,7 +421,7 @@ def moe_ffn_s8_forward(f: moe_ffn_s8, x, T: int, y, workspace=None, stream=None)
     xp, lx = _rows(x, T, f.d_model, f.torch_dtype, "x")
     yp, ly = _rows(y, T, f.d_model, f.torch_dtype, "y")
     wp, wn = _space(workspace)
-    _check(lib.moe_ffn_s8_forward(f.ref, xp, lx, T, yp, ly, wp, wn, _stream(stream)),
+    _check(lib.moe_ffn_s8_forward(f.ref, xp, lx, _int(T), yp, ly, wp, wn, _stream(stream)),
            "moe_ffn_s8_forward")
 
 

@@ -19,6 +19,60 @@ def test_product_refuses_more_columns_than_its_indices_hold(T, N):
     assert st == capi.MOE_ERR_UNSUPPORTED and "N" in capi.last_error()
 
 
+class Huge:
+    """What the binding looks at of a CUDA tensor of any size."""
+    is_cuda = True
+
+    def __init__(self, *shape, dtype=torch.bfloat16):
+        self.shape, self.dtype = torch.Size(shape), dtype
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return P
+
+
+BIG = (1 << 32) + 4     # 4 in 32 bits
+
+
+def test_binding_passes_no_size_cut_to_32_bits():
+    """Sizes above 2^31 are refused as those above 2^30 are; a size taken modulo 2^32 would be answered in part."""
+    i8, f32 = torch.int8, torch.float32
+
+    def refused(call):
+        with pytest.raises(capi.MoeError) as e:
+            call()
+        assert e.value.status == capi.MOE_ERR_UNSUPPORTED
+
+    refused(lambda: capi.moe_quantize_s8(Huge(BIG, 1), Huge(BIG, 1, dtype=i8), Huge(BIG, dtype=f32)))
+    refused(lambda: capi.moe_quantize_s8(Huge(1, BIG), Huge(1, BIG, dtype=i8), Huge(1, dtype=f32)))
+
+    def product(T, N, K):
+        return lambda: capi.moe_matmul_s8(Huge(T, K, dtype=i8), Huge(T, dtype=f32), Huge(N, K, dtype=i8),
+                                          Huge(N, dtype=f32), Huge(T, N))
+    refused(product(BIG, 8, 16))
+    refused(product(2, BIG + 4, 16))
+    refused(product(2, 8, BIG + 12))
+    f = capi.make_ffn(Huge(16, 8), Huge(16, 8), Huge(8, 16))
+    x, h = Huge(BIG, 8), Huge(BIG, 16)
+    refused(lambda: capi.moe_ffn_forward(f, x, BIG, x))
+    refused(lambda: capi.moe_ffn_backward(f, x, h, h, x, BIG, x))
+    with pytest.raises(capi.MoeError):
+        capi.moe_ffn_forward(f, x, 4 - (1 << 32), x)
+    w, s = Huge(16, 16, dtype=i8), Huge(16, dtype=f32)
+    f8 = capi.make_ffn_s8(w, s, w, s, w, s, "silu", torch.bfloat16)
+    refused(lambda: capi.moe_ffn_s8_forward(f8, Huge(BIG, 16), BIG, Huge(BIG, 16)))
+    # the workspace of more rows than there are 32-bit sizes is no smaller than that of 2^31 - 1
+    top = (1 << 31) - 1
+    assert capi.moe_ffn_workspace(f, BIG, True) == capi.moe_ffn_workspace(f, top, True)
+    assert capi.moe_ffn_s8_workspace(f8, BIG) == capi.moe_ffn_s8_workspace(f8, top)
+    # widths: refused when the handle is used
+    wide = BIG + 4
+    f = capi.make_ffn(Huge(wide, 8), Huge(wide, 8), Huge(8, wide))
+    refused(lambda: capi.moe_ffn_workspace(f, 4))
+
+
 # ---- rows whose scale is a small subnormal number ----------------------------------------------------------------
 
 UNIT = 2.0 ** -149      # fp32's smallest positive number
