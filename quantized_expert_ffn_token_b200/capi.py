@@ -321,13 +321,12 @@ def make_ffn(w_gate, w_up, w_down, act="silu") -> moe_ffn:
     f.w_up = _full(w_up, (I, d), f.torch_dtype, "w_up")
     f.w_down = _full(w_down, (d, I), f.torch_dtype, "w_down")
     f.keep = (w_gate, w_up, w_down)
-    f.ref = ctypes.byref(f)
     return f
 
 
 def moe_ffn_workspace(f: moe_ffn, T: int, backward: bool = False) -> int:
     n = ctypes.c_longlong()
-    _check(lib.moe_ffn_workspace(f.ref, _int(T), 1 if backward else 0, ctypes.byref(n)), "moe_ffn_workspace")
+    _check(lib.moe_ffn_workspace(f, _int(T), 1 if backward else 0, ctypes.byref(n)), "moe_ffn_workspace")
     return n.value
 
 
@@ -338,7 +337,7 @@ def moe_ffn_forward(f: moe_ffn, x, T: int, y, gate=None, up=None, workspace=None
     gp = None if gate is None else _full(gate, (T, I), dt, "gate")
     up_ = None if up is None else _full(up, (T, I), dt, "up")
     wp, wn = _space(workspace)
-    _check(lib.moe_ffn_forward(f.ref, xp, lx, _int(T), yp, ly, gp, up_, wp, wn, _stream(stream)),
+    _check(lib.moe_ffn_forward(f, xp, lx, _int(T), yp, ly, gp, up_, wp, wn, _stream(stream)),
            "moe_ffn_forward")
 
 
@@ -359,7 +358,7 @@ def moe_ffn_backward(f: moe_ffn, x, gate, up, dy, T: int, dx=None, dw_gate=None,
     du = None if dw_up is None else _full(dw_up, (I, d), wdt, "dw_up")
     dd = None if dw_down is None else _full(dw_down, (d, I), wdt, "dw_down")
     wp, wn = _space(workspace)
-    _check(lib.moe_ffn_backward(f.ref, xp, lx, gp, up_, dyp, ldy, _int(T), dxp, ldx, dg, du, dd, flags, wp, wn,
+    _check(lib.moe_ffn_backward(f, xp, lx, gp, up_, dyp, ldy, _int(T), dxp, ldx, dg, du, dd, flags, wp, wn,
                                 _stream(stream)), "moe_ffn_backward")
 
 
@@ -407,13 +406,12 @@ def make_ffn_s8(w_gate, s_gate, w_up, s_up, w_down, s_down, act="silu", dtype=No
     f.w_up, f.s_up = _codes(w_up, (I, d), "w_up"), _scales(s_up, I, "s_up")
     f.w_down, f.s_down = _codes(w_down, (d, I), "w_down"), _scales(s_down, d, "s_down")
     f.keep = (w_gate, s_gate, w_up, s_up, w_down, s_down)
-    f.ref = ctypes.byref(f)
     return f
 
 
 def moe_ffn_s8_workspace(f: moe_ffn_s8, T: int) -> int:
     n = ctypes.c_longlong()
-    _check(lib.moe_ffn_s8_workspace(f.ref, _int(T), ctypes.byref(n)), "moe_ffn_s8_workspace")
+    _check(lib.moe_ffn_s8_workspace(f, _int(T), ctypes.byref(n)), "moe_ffn_s8_workspace")
     return n.value
 
 
@@ -421,7 +419,7 @@ def moe_ffn_s8_forward(f: moe_ffn_s8, x, T: int, y, workspace=None, stream=None)
     xp, lx = _rows(x, T, f.d_model, f.torch_dtype, "x")
     yp, ly = _rows(y, T, f.d_model, f.torch_dtype, "y")
     wp, wn = _space(workspace)
-    _check(lib.moe_ffn_s8_forward(f.ref, xp, lx, _int(T), yp, ly, wp, wn, _stream(stream)),
+    _check(lib.moe_ffn_s8_forward(f, xp, lx, _int(T), yp, ly, wp, wn, _stream(stream)),
            "moe_ffn_s8_forward")
 
 

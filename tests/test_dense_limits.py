@@ -1,5 +1,8 @@
 """Dense feed-forward operators at the ends of their ranges: what the calls document, at the values and sizes where
 it is easiest to break."""
+import gc
+import weakref
+
 import pytest
 import torch
 
@@ -71,6 +74,30 @@ def test_binding_passes_no_size_cut_to_32_bits():
     wide = BIG + 4
     f = capi.make_ffn(Huge(wide, 8), Huge(wide, 8), Huge(8, wide))
     refused(lambda: capi.moe_ffn_workspace(f, 4))
+
+
+# ---- handles ------------------------------------------------------------------------------------------------------
+
+def test_a_handle_frees_its_weights_with_its_last_reference():
+    """A handle keeps its weights alive, and gives them up at once: the cyclic collector does not see device memory, so
+    a handle per training step must not wait for it."""
+    i8, f32 = torch.int8, torch.float32
+    w = [Huge(16, 16) for _ in range(3)]
+    q = [t for _ in range(3) for t in (Huge(16, 16, dtype=i8), Huge(16, dtype=f32))]
+    gc.collect()
+    gc.disable()
+    try:
+        for tensors, make in ((w, lambda: capi.make_ffn(*w)),
+                              (q, lambda: capi.make_ffn_s8(*q, "silu", torch.bfloat16))):
+            watch = [weakref.ref(t) for t in tensors]
+            f = make()
+            tensors.clear()
+            assert all(r() is not None for r in watch)
+            assert (capi.moe_ffn_workspace if tensors is w else capi.moe_ffn_s8_workspace)(f, 4) > 0
+            del f
+            assert all(r() is None for r in watch)
+    finally:
+        gc.enable()
 
 
 # ---- rows whose scale is a small subnormal number ----------------------------------------------------------------
