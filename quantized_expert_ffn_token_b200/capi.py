@@ -12,8 +12,6 @@ from __future__ import annotations
 import ctypes
 import os
 
-import torch
-
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libqeffn.so")
 
@@ -45,7 +43,6 @@ MOE_ACT_GELU_TANH = 2
 MOE_ACT_GELU = 3
 MOE_FFN_GRAD_FP32 = 1
 MOE_FFN_GRAD_ADD = 2
-DTYPES = {torch.bfloat16: MOE_BF16, torch.float16: MOE_FP16, torch.float32: MOE_FP32}
 ACTS = {"silu": MOE_ACT_SILU, "gelu_tanh": MOE_ACT_GELU_TANH, "gelu": MOE_ACT_GELU}
 FORMATS = {"q4": MOE_Q4B32, "q3": MOE_Q3B32, "q2": MOE_Q2B32}
 
@@ -262,6 +259,25 @@ def make_record(x=None, y=None, y_f32=None, ids=None, w=None, rows=None) -> moe_
 # Tensors carry their sizes here: activations are 2-d CUDA tensors whose rows may lie apart (a slice of a wider
 # buffer); everything else is contiguous.  Shapes and types are checked before an address leaves Python.
 
+class _TorchTypes:
+    """torch's types, looked up when a tensor first comes: the binding itself needs no torch."""
+
+    def __getattr__(self, name):      # called until the attributes are there
+        import torch
+        self.int8, self.float32 = torch.int8, torch.float32
+        self.dtypes = {torch.bfloat16: MOE_BF16, torch.float16: MOE_FP16, torch.float32: MOE_FP32}
+        return object.__getattribute__(self, name)
+
+
+_types = _TorchTypes()
+
+
+def __getattr__(name):
+    if name == "DTYPES":              # moe_dtype of a torch dtype
+        return _types.dtypes
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
 def _int(n: int) -> int:
     """n as a C int.  ctypes takes a size modulo 2^32; past its range it becomes the nearest C int, which is
     outside every call's limits."""
@@ -270,7 +286,7 @@ def _int(n: int) -> int:
 
 def _dtype(t) -> int:
     try:
-        return DTYPES[t.dtype]
+        return _types.dtypes[t.dtype]
     except KeyError:
         raise ValueError(f"dtype {t.dtype}: bf16, fp16 or fp32 expected") from None
 
@@ -363,11 +379,11 @@ def moe_ffn_backward(f: moe_ffn, x, gate, up, dy, T: int, dx=None, dw_gate=None,
 
 
 def _codes(t, shape, what: str):
-    return _full(t, shape, torch.int8, what)
+    return _full(t, shape, _types.int8, what)
 
 
 def _scales(t, n: int, what: str):
-    return _full(t, (n,), torch.float32, what)
+    return _full(t, (n,), _types.float32, what)
 
 
 def moe_quantize_s8(x, q, scale, stream=None) -> None:
@@ -400,7 +416,7 @@ def make_ffn_s8(w_gate, s_gate, w_up, s_up, w_down, s_down, act="silu", dtype=No
     """The block over 8-bit weights and their row scales; ``dtype``: torch.bfloat16 or torch.float16 of x and y."""
     I, d = w_gate.shape
     f = moe_ffn_s8()
-    f.d_model, f.d_ff, f.dtype, f.act = _int(d), _int(I), DTYPES.get(dtype, 0), _act(act)
+    f.d_model, f.d_ff, f.dtype, f.act = _int(d), _int(I), _types.dtypes.get(dtype, 0), _act(act)
     f.torch_dtype = dtype
     f.w_gate, f.s_gate = _codes(w_gate, (I, d), "w_gate"), _scales(s_gate, I, "s_gate")
     f.w_up, f.s_up = _codes(w_up, (I, d), "w_up"), _scales(s_up, I, "s_up")

@@ -1,12 +1,17 @@
 """Dense feed-forward operators at the ends of their ranges: what the calls document, at the values and sizes where
 it is easiest to break."""
 import gc
+import os
+import subprocess
+import sys
 import weakref
 
 import pytest
 import torch
 
 from quantized_expert_ffn_token_b200 import capi
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 # ---- sizes: refused before a device is touched -------------------------------------------------------------------
@@ -98,6 +103,24 @@ def test_a_handle_frees_its_weights_with_its_last_reference():
             assert all(r() is None for r in watch)
     finally:
         gc.enable()
+
+
+# ---- the binding without torch ------------------------------------------------------------------------------------
+
+def test_binding_imports_without_torch():
+    """The binding is ctypes: a program that passes addresses needs no torch, and pays for no import of it."""
+    code = """
+import ctypes, sys
+sys.modules["torch"] = None          # importing it raises ImportError
+from quantized_expert_ffn_token_b200 import capi
+assert capi.lib.moe_quantize_s8(None, capi.MOE_BF16, 0, 4, 8, None, None, None) == capi.MOE_ERR_INVALID_ARG
+h = ctypes.c_void_p()
+assert capi.lib.moe_create(None, 0, ctypes.byref(h)) == capi.MOE_ERR_INVALID_ARG
+print(sorted(capi.EXPORTED)[0])
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, cwd=ROOT)
+    assert r.returncode == 0 and r.stdout.startswith("moe_"), r.stderr[-2000:]
+    assert capi.DTYPES == {torch.bfloat16: capi.MOE_BF16, torch.float16: capi.MOE_FP16, torch.float32: capi.MOE_FP32}
 
 
 # ---- rows whose scale is a small subnormal number ----------------------------------------------------------------
