@@ -65,6 +65,7 @@ struct TileArgs {
     int W, subs;                // sub-tile width, sub-tiles per tile
     int splits, kper;           // reduction splits (CTAs or pairs of a cluster), k steps each
     int stages, stage_bytes, b_bytes;   // b_bytes: a sub-tile's B in one CTA
+    long long tile_wait;        // limit of the epilogue's wait for a tile, see tile_wait_cycles()
     int act;
     int fp16;                   // 16-bit operands (and out1, out2): fp16 rather than bf16
     int one_out;                // one output a tile: two store tiles take turns
@@ -550,7 +551,7 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
                             prefetch_l2((const uint16_t *)p.in2 + at + c);
                         }
                     }
-                if (!mbar_wait(&bar->acc_full[slot], use & 1)) break;
+                if (!mbar_wait(&bar->acc_full[slot], use & 1, false, p.tile_wait)) break;
                 tc_fence_after();
                 const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + GT_W * slot;
                 for (int sub = 0; sub < p.subs; ++sub)
@@ -569,7 +570,7 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
         const int g = tile_at(order.at(0), m0, n0);
         const Product &pr = p.prod[g];
         m0 += rank * 128 + 32 * q;
-        if (warp >= GT_EPI_W0 && mbar_wait(&bar->acc_full[0], 0)) {
+        if (warp >= GT_EPI_W0 && mbar_wait(&bar->acc_full[0], 0, false, p.tile_wait)) {
             tc_fence_after();
             for (int c = 32 * team; c < W * p.subs; c += 64) {
                 uint32_t r[32];
@@ -832,6 +833,7 @@ template <int NG>
 void set_shape(const GemmArgs &g, const Shape &sh, int ksteps, TileArgs<NG> &p) {
     p.W = sh.W, p.subs = sh.subs, p.splits = sh.splits;
     p.kper = (ksteps + sh.splits - 1) / sh.splits;
+    p.tile_wait = tile_wait_cycles(p.kper);
     p.b_bytes = b_rows(g.b_mn, sh.W, sh.cg) * GT_KB;
     p.stage_bytes = GT_A + sh.subs * p.b_bytes;
     p.stages = std::min(GT_MAX_STAGES, GT_RING / p.stage_bytes);

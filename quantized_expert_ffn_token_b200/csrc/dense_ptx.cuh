@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <stdint.h>
 
+#include "dense_schedule.cuh"
 #include "moe.h"
 
 namespace qeffn {
@@ -12,8 +13,6 @@ namespace dense {
 // Error word of the dense kernels, one per device: set by a bounded wait that ran out.  (Kernels with waits are all in
 // the one source file that includes this header.)
 static __device__ int g_error;
-
-constexpr long long kSpinCycles = 4000000000LL;   // clock64 cycles, about two seconds
 
 __device__ __forceinline__ uint32_t su32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
@@ -31,14 +30,14 @@ __device__ __forceinline__ bool mbar_try(uint64_t *b, uint32_t parity) {
 }
 // Bounded wait; false when it ran out (the error word is set) or another CTA reported an error.  With `drain` it
 // goes on after errors elsewhere: for work in flight, which always completes.
-__device__ __forceinline__ bool mbar_wait(uint64_t *b, uint32_t parity, bool drain = false) {
+__device__ __forceinline__ bool mbar_wait(uint64_t *b, uint32_t parity, bool drain = false, long long limit = kSpinCycles) {
     if (mbar_try(b, parity)) return true;
     const long long t0 = clock64();
     for (int it = 0;; ++it) {
         if (mbar_try(b, parity)) return true;
         if ((it & 63) == 63) {
             if (!drain && *(volatile int *)&g_error != 0) return false;
-            if (clock64() - t0 > kSpinCycles) {
+            if (clock64() - t0 > limit) {
                 atomicCAS(&g_error, 0, MOE_ERR_DEVICE_TIMEOUT);
                 return false;
             }

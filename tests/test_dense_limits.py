@@ -2,6 +2,7 @@
 it is easiest to break."""
 import gc
 import os
+import shutil
 import subprocess
 import sys
 import weakref
@@ -10,6 +11,7 @@ import pytest
 import torch
 
 from quantized_expert_ffn_token_b200 import capi
+from tests.test_dense_ffn import check_backward
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -81,6 +83,32 @@ def test_binding_passes_no_size_cut_to_32_bits():
     refused(lambda: capi.moe_ffn_workspace(f, 4))
 
 
+# ---- bounded waits -------------------------------------------------------------------------------------------------
+
+def _host_program(tmp_path, body):
+    """Compiles and runs host code over the kernels' schedule header; its output's lines."""
+    nvcc = shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
+    if not os.path.exists(nvcc):
+        pytest.skip("nvcc not available")
+    src, exe = tmp_path / "schedule.cu", tmp_path / "schedule"
+    src.write_text('#include <stdio.h>\n#include "dense_schedule.cuh"\nusing namespace qeffn::dense;\n' + body)
+    csrc = os.path.join(ROOT, "quantized_expert_ffn_token_b200", "csrc")
+    subprocess.check_call([nvcc, "-std=c++17", "-I", csrc, "-o", str(exe), str(src)])
+    return subprocess.check_output([str(exe)], text=True).splitlines()
+
+
+def test_wait_for_a_tile_outlasts_its_reduction(tmp_path):
+    """The epilogue waits for a tile's whole reduction at once.  Weight gradients reduce over up to 2^30 rows, 64 a step;
+    a step on a CTA pair with 128 columns takes at least 256 cycles (128 rows x 64 values x 1 column in 2) and is modelled
+    at 1.18 * 345 = 408.  The limit leaves twice that at every length, and stays near two seconds for the usual ones."""
+    steps = [1, 128, 1 << 13, 1 << 20, 1 << 24]
+    out = _host_program(tmp_path, "int main() { for (long long k : {%s}) printf(\"%%lld\\n\", tile_wait_cycles(k)); }"
+                        % ", ".join(f"{k}LL" for k in steps))
+    for k, limit in zip(steps, map(int, out)):
+        assert limit >= 2 * 408 * k
+    assert int(out[1]) < 4.01e9
+
+
 # ---- handles ------------------------------------------------------------------------------------------------------
 
 def test_a_handle_frees_its_weights_with_its_last_reference():
@@ -150,3 +178,30 @@ def test_codes_of_tiny_rows_stay_in_range(cols):
     capi.moe_quantize_s8(x.cuda(), q, scale)
     assert torch.equal(scale.double().cpu(), s * UNIT)
     assert torch.equal(q.cpu().double(), want)
+
+
+# ---- the largest number of rows ----------------------------------------------------------------------------------
+
+@pytest.mark.gpu
+def test_weight_gradients_over_the_largest_batch():
+    """2^30 rows, all zero but for some in front, in the middle and at the end: the gradients are those of these rows
+    alone (a row of zeros adds exact zeros), and no wait gives up on the way.  Inputs may share memory: x is dy and gate
+    is up, which keeps the test below 90 GB."""
+    T, d, I, dt = 1 << 30, 8, 8, torch.bfloat16
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 100e9:
+        pytest.skip("needs 100 GB of device memory")
+    gen = torch.Generator(device="cuda").manual_seed(30)
+    rnd = lambda *s: torch.randn(*s, generator=gen, device="cuda").to(dt)  # noqa: E731
+    wg, wu, wd = rnd(I, d), rnd(I, d), rnd(d, I)
+    x, g = torch.zeros(T, d, dtype=dt, device="cuda"), torch.zeros(T, I, dtype=dt, device="cuda")
+    at = torch.cat([torch.arange(s, s + 40, device="cuda") for s in (0, 12345, T // 2 - 20, 3 * (T // 4), T - 40)])
+    x[at], g[at] = rnd(at.numel(), d), rnd(at.numel(), I)
+    f = capi.make_ffn(wg, wu, wd)
+    ws = torch.empty(capi.moe_ffn_workspace(f, T, True), dtype=torch.uint8, device="cuda")
+    out = [torch.full(s, float("nan"), device="cuda") for s in ((I, d), (I, d), (d, I))]
+    capi.moe_ffn_backward(f, x, g, g, x, T, None, *out, workspace=ws)
+    assert capi.moe_ffn_get_device_error() == 0
+    check_backward(x[at], g[at], g[at], x[at], wg, wu, wd, "silu", [None] + out, dw_dtype=torch.float32)
+    del x, g, ws
+    torch.cuda.empty_cache()
