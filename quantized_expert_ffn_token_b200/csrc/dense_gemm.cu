@@ -75,35 +75,6 @@ struct TileArgs {
     const float *row_scale, *col_scale0, *col_scale1, *bias;
 };
 
-// The tiles of cluster c of P, in order.  The first `big` tiles (a product with a long reduction) are dealt round robin;
-// so the first big % P clusters hold one more of them, and the others take `rounds` more of the remaining tiles, which
-// are dealt round robin among those that have time.
-template <int NG>
-struct Order {
-    int c, P, n, mine, rest, rounds;
-    bool more;
-    __device__ Order(const TileArgs<NG> &p, int cluster, int clusters) : c(cluster), P(clusters), n(p.tiles) {
-        if constexpr (NG > 1) {
-            mine = c < p.big ? (p.big - c + P - 1) / P : 0;
-            const int r = p.big % P;
-            rest = P - r;
-            more = c >= r;
-            rounds = p.rounds;
-            big = p.big;
-        }
-    }
-    int big = 0;
-    __device__ int at(int k) const {   // -1: no more
-        int t = c + k * P;
-        if constexpr (NG > 1)
-            if (k >= mine) {
-                const int j = k - mine;
-                t = big + (more && j < rounds ? j * rest + c - (P - rest) : rounds * rest + (j - (more ? rounds : 0)) * P + c);
-            }
-        return t < n ? t : -1;
-    }
-};
-
 struct GtBars {
     uint64_t full[GT_MAX_STAGES], empty[GT_MAX_STAGES], acc_full[2], acc_empty[2], mma_done;
     uint32_t tmem;
@@ -244,7 +215,7 @@ __global__ void __launch_bounds__(GT_NT, 1) k_gemm_tc(const __grid_constant__ Ma
     if (CG * p.splits > 1) cluster_sync();
     tc_fence_after();
     const uint32_t tmem = bar->tmem;
-    const Order<NG> order(p, blockIdx.x / (CG * p.splits), gridDim.x / (CG * p.splits));
+    const Order<(NG > 1)> order(p.tiles, p.big, p.rounds, blockIdx.x / (CG * p.splits), gridDim.x / (CG * p.splits));
     // tiles of a product in bands of 8 row blocks, so that the tiles in flight share rows of both operands in L2
     auto tile_at = [&](int t, int &m0, int &n0) {
         int g = 0;

@@ -2,6 +2,7 @@
 it is easiest to break."""
 import gc
 import os
+import random
 import shutil
 import subprocess
 import sys
@@ -107,6 +108,47 @@ def test_wait_for_a_tile_outlasts_its_reduction(tmp_path):
     for k, limit in zip(steps, map(int, out)):
         assert limit >= 2 * 408 * k
     assert int(out[1]) < 4.01e9
+
+
+# ---- the order of tiles -----------------------------------------------------------------------------------------------
+
+def test_every_tile_is_dealt_once(tmp_path):
+    """The kernels' own order, run on the host: over all clusters every tile comes once and ascending, the tiles of the
+    long product first and evenly, and a cluster with one long tile less takes the extra rounds of short ones."""
+    rng = random.Random(5)
+    cases = []
+    for _ in range(1500):
+        big, small = rng.choice([0, rng.randrange(200)]), rng.randrange(800)
+        P = rng.randint(1, min(74, max(1, big + small)))
+        r = big % P
+        rounds = rng.randint(0, small // (P - r)) if r else 0
+        cases.append((big + small, big, rounds, P))
+    rows = ", ".join("{%d, %d, %d, %d}" % c for c in cases)
+    out = _host_program(tmp_path, """
+template <bool G> void deal(const int *q) {
+    for (int c = 0; c < q[3]; ++c) {
+        Order<G> order(q[0], q[1], q[2], c, q[3]);
+        int k = 0;
+        for (int t; (t = order.at(k)) >= 0 && k <= q[0]; ++k) printf("%%d ", t);
+        printf("\\n");
+    }
+}
+int main() {
+    static const int q[][4] = {%s};
+    for (const int *p : q) deal<true>(p), deal<false>(p);
+}
+""" % rows)
+    lines = iter(out)
+    for n, big, rounds, P in cases:
+        group = [list(map(int, next(lines).split())) for _ in range(P)]
+        single = [list(map(int, next(lines).split())) for _ in range(P)]
+        for dealt in (group, single):
+            assert sorted(t for d in dealt for t in d) == list(range(n))
+            assert all(d == sorted(d) for d in dealt)
+        long = [sum(t < big for t in d) for d in group]
+        assert max(long) - min(long) <= 1
+        if big % P:
+            assert min(len(d) - m for d, m in zip(group, long) if m == min(long)) >= rounds
 
 
 # ---- handles ------------------------------------------------------------------------------------------------------
