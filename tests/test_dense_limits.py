@@ -12,7 +12,7 @@ import pytest
 import torch
 
 from quantized_expert_ffn_token_b200 import capi
-from tests.test_dense_ffn import check_backward
+from tests.test_dense_ffn import _backward, _forward, _mk, _ws, check_backward, quantize64
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -247,3 +247,79 @@ def test_weight_gradients_over_the_largest_batch():
     check_backward(x[at], g[at], g[at], x[at], wg, wu, wd, "silu", [None] + out, dw_dtype=torch.float32)
     del x, g, ws
     torch.cuda.empty_cache()
+
+
+# ---- padding ---------------------------------------------------------------------------------------------------------
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 13, 31, 129, 333])
+def test_nothing_outside_the_batch_is_read(T):
+    """A padded batch: NaN in the rows behind the last one and in the columns beside x and dy changes nothing, and the
+    padding of the outputs stays as it is."""
+    d, I, dt = 136, 264, torch.bfloat16
+    x, wg, wu, wd, dy, rnd = _mk(T, T, d, I, dt)
+    f = capi.make_ffn(wg, wu, wd)
+    y, g, u = _forward(f, x)
+    want = _backward(f, x, g, u, dy)
+
+    def padded(v):
+        buf = torch.full((T + 9, d + 24), float("nan"), dtype=v.dtype, device="cuda")
+        buf[:T, 8:8 + d] = v
+        return buf, buf[:, 8:8 + d]
+
+    def unchanged(buf, v):
+        return torch.equal(buf[:T, 8:8 + d], v) and bool(buf[T:].isnan().all() and buf[:, :8].isnan().all()
+                                                          and buf[:, 8 + d:].isnan().all())
+
+    (_, xp), (_, dyp), (yb, yp), (dxb, dxp) = padded(x), padded(dy), padded(y * 0), padded(y * 0)
+    capi.moe_ffn_forward(f, xp, T, yp, workspace=_ws(capi.moe_ffn_workspace(f, T)))
+    assert unchanged(yb, y)
+    dw = [torch.full_like(v, float("nan")) for v in want[1:]]
+    capi.moe_ffn_backward(f, xp, g, u, dyp, T, dxp, *dw, workspace=_ws(capi.moe_ffn_workspace(f, T, True)))
+    assert unchanged(dxb, want[0])
+    assert all(torch.equal(p, q) for p, q in zip(dw, want[1:]))
+
+
+# ---- graphs ----------------------------------------------------------------------------------------------------------
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [3, 200])
+def test_captured_between_copies_and_on_two_streams(T):
+    """A graph whose calls come after a copy and a fill, run in two branches (a workspace each) and join again, replayed
+    on other inputs; and two such graphs in flight at once."""
+    d, I, dt = 256, 512, torch.bfloat16
+    graphs = []
+    for seed in (1, 2):
+        x, wg, wu, wd, dy, rnd = _mk(seed, T, d, I, dt)
+        f = capi.make_ffn(wg, wu, wd)
+        src, y, g, u = torch.empty_like(x), torch.empty_like(x), x.new_empty(T, I), x.new_empty(T, I)
+        q, s = torch.empty(T, d, dtype=torch.int8, device="cuda"), torch.empty(T, device="cuda")
+        out = [torch.empty_like(v) for v in (x, wg, wu, wd)]
+        ws = _ws(capi.moe_ffn_workspace(f, T)), _ws(capi.moe_ffn_workspace(f, T, True))
+        a, b = torch.cuda.Stream(), torch.cuda.Stream()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=a):
+            x.copy_(src)                      # a copy node, then a kernel of torch's, then the block
+            y.zero_()
+            capi.moe_ffn_forward(f, x, T, y, g, u, ws[0], a)
+            b.wait_stream(a)
+            capi.moe_quantize_s8(y, q, s, b)
+            capi.moe_ffn_backward(f, x, g, u, y, T, *out, workspace=ws[1], stream=a)
+            a.wait_stream(b)
+        graphs.append((graph, f, src, x, y, g, u, q, s, out, rnd, a, (wg, wu, wd), ws))
+    for _ in range(3):
+        for graph, f, src, *_ in graphs:
+            src.copy_(torch.randn_like(src.float()))
+        torch.cuda.synchronize()
+        for graph, *_, a, _, _ in graphs:
+            with torch.cuda.stream(a):
+                graph.replay()
+        torch.cuda.synchronize()
+        for graph, f, src, x, y, g, u, q, s, out, rnd, a, w, ws in graphs:
+            y2, g2, u2 = _forward(f, src)
+            assert torch.equal(y, y2) and torch.equal(g, g2) and torch.equal(u, u2)
+            assert all(torch.equal(p, r) for p, r in zip(out, _backward(f, src, g2, u2, y2)))
+            q64, s64 = quantize64(y2)
+            assert torch.equal(q.double(), q64) and torch.equal(s.double(), s64)
+    assert capi.moe_ffn_get_device_error() == 0
