@@ -374,8 +374,9 @@ MOE_API int moe_quantize_s8(const void *x, int dtype, long long ld_x, int rows, 
 /* y[t][n] = (a_scale[t] * w_scale[n]) * sum_k a[t][k] w[n][k]  (+ bias[n]),
  * a [T][K] and w [N][K] contiguous 8-bit codes, scales and bias fp32, y
  * [T][N] in y_dtype (any moe_dtype).  The sum is exact in int32; then fp32,
- * rounded once.  Limits: K a multiple of 16 up to 65536, N a multiple of 8 up to
- * 2^30.  T == 0 is a no-op. */
+ * rounded once.  The workspace is 0 bytes at present (NULL will do).  Limits:
+ * K a multiple of 16 up to 65536, N a multiple of 8 up to 2^30.  T == 0 is a
+ * no-op. */
 MOE_API int moe_matmul_s8_workspace(int T, int N, int K, long long *bytes);
 MOE_API int moe_matmul_s8(const int8_t *a, const float *a_scale, int T, const int8_t *w, const float *w_scale, int N,
                           int K, const float *bias, void *y, int y_dtype, long long ld_y, void *workspace,
@@ -404,7 +405,9 @@ MOE_API int moe_ffn_s8_forward(const moe_ffn_s8 *f, const void *x, long long ld_
 /* Read (and clear) the error word of the calls above on the current device
  * (their kernels' bounded waits set it; *code receives 0 or a MOE_ERR_*
  * value).  After a nonzero code the results since the last call of this are
- * undefined.  Synchronises the device. */
+ * undefined: from the wait that ran out until the word is read, kernels that
+ * would wait leave at once, and the calls still return MOE_OK.  Synchronises
+ * the device. */
 MOE_API int moe_ffn_get_device_error(int *code);
 
 /* Static text for a status code. */

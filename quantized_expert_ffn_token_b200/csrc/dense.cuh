@@ -62,8 +62,10 @@ int launch_quantize_s8(const void *x, int dtype, long long ld, int rows, int col
 
 // act(z) and act'(z).  With P(z) the gate's weight (a sigmoid, or the normal
 // distribution function), act = z P and act' = P + z P'.  The fast exponential
-// and division (a few fp32 ulp) are far inside the 16-bit or 8-bit rounding
-// that follows.
+// and division are off by a few fp32 ulp (the exponential by |x| ulp at large
+// arguments), far inside the 16-bit or 8-bit rounding that follows.  The
+// division gives 0 once its divisor is above 2^126: silu(z) is 0 below
+// z = -87.3, where it is smaller than 1e-36.
 __device__ __forceinline__ float fast_sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
 
 constexpr float kGeluC = 1.5957691216057308f;   // 2 sqrt(2/pi): (1 + tanh v)/2 is the sigmoid of 2 v

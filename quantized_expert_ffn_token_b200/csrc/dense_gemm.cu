@@ -688,7 +688,9 @@ int k_steps(const GemmArgs &g) {
 // tile's epilogue takes 2820 cycles and 14 a column (the gate's gradient, with its loads, 56), hidden behind the next
 // tile where there is one; a split adds the exchange, 2400 cycles, 32 a column and 266 a CTA of the cluster; a pair 1770
 // to start.  Fitted to 6,700 timings of 118 products (24 to 2,200 rows) on B200: the chosen shape is on average 1.4 % and
-// at most 15 % slower than the fastest one.
+// at most 15 % slower than the fastest one; outside that range it extrapolates.  It knows neither the kind of
+// activation (the gate's epilogue takes longer for the erf form: 8-bit block, 8192 rows of 640 x 7680, 311 us against 215
+// with SiLU) nor HBM.
 int choose(const GemmArgs &g, Shape *best, long long *time) {
     const int ksteps = k_steps(g);
     long long least = -1;
@@ -731,7 +733,9 @@ constexpr long long kLaunchCycles = 7600;   // a launch's own, in the models
 
 // The same for products in one launch (16-bit, B's row index contiguous, stored plainly; pairs, one sub-tile), and the
 // order of its tiles.  `big`: the first one's reduction is longer and its tiles go first.  Back to back, a k step takes
-// 1.18 times the above and a tile 500 cycles more, or its share of HBM's write rate (1800 cycles and 5 a column).
+// 1.18 times the above and a tile 500 cycles more, or its share of HBM's write rate (1800 cycles and 5 a column).  The
+// reduction is not split: narrow matrices with many rows leave most pairs without a tile (backward pass, 8192 rows of
+// 256 x 256: 6 tiles of weight gradients, 51 us for a floor of 4).
 int choose_group(const GemmArgs *g, int n, bool big, Shape *best, int *rounds, long long *time) {
     long long least = -1;
     int room = 0;

@@ -217,8 +217,10 @@ int launch_rows_type(const RowsArgs &p, bool gate, cudaStream_t st) {
 
 }  // namespace
 
-// Which products these are.  Up to 16 rows always; up to 32 while the weights are few, where the launch counts: a 512 x
-// 512 block at 32 rows took 4.4 us (tensor-core tiles 8.5), 1024 x 2048 9.9 (12.9), 2560 x 10240 51 (38).
+// Which products these are.  Up to 16 rows always; up to 32 while the weights are few, where the launch counts.  A bf16
+// block at 32 rows, us: 512 x 512 4.5 (tensor-core tiles 8.6), 1024 x 2048 8.4 (13.7), 2560 x 5120 32 (26), 2560 x 10240 56
+// (39).  The limit is a product's, not the block's: 2048 x 4096 tiles its gate and up and streams its down projection,
+// 29 (22 with both streamed).
 bool rows_fit(const GemmArgs &g) {
     if (g.a_mn || g.b_mn || g.segs != 1) return false;
     const long long bytes = (long long)g.N * g.K * (g.type == DT_S8 ? 1 : 2) * (g.epi == EPI_GATE ? 2 : 1);
