@@ -3,7 +3,7 @@
 // Bound by HBM: a row is read once into registers (16-byte loads), reduced over the CTA, scaled and written.  Rows whose
 // address does not allow 16-byte accesses are read twice, the second time from L1/L2.  With 16 loads a thread a part of
 // the row goes through local memory instead (a 1024-thread CTA's 64 registers a thread spill 340 bytes, 512 threads' 128
-// spill 60): rows of more than 4096 loads while there are at most 148 of them, of more than 3072 loads otherwise.
+// spill 60): rows of more than 4096 loads while there are at most 148 of them, and those too long for 8 loads of 384 threads otherwise.
 // The codes are those of correctly rounded divisions, so that they are the same wherever they are computed: the product
 // with a reciprocal decides where it lies 1e-4 or more from a half (its error is below 127 * 2^-21), a division the rest.
 #include "dense.cuh"
